@@ -445,6 +445,106 @@ sb_status sb_tdc_refresh_fp8(const void* x, const void* y, uint8_t* codes, float
 sb_status sb_tdc_reuse_fp8(const void* x, const uint8_t* codes, const float* scale, void* y, int64_t M, int64_t C,
                            const sb_module_state* state, sb_stream stream);
 
+/* ---- 8-bit floating point with one power-of-two scale per block ---------------------------------
+ * The precision between INT8 / NVFP4 and BF16 that needs no rotation and no tensor-wide statistics:
+ * E4M3 codes, and for each block the E8M0 byte e + 127 of the smallest power of two 2^e with
+ * max |x| <= 448 * 2^e over the block (0 for a block of zeros); code = E4M3(RN(x * 2^-e)),
+ * value = code * 2^e. A power of two makes the scaling exact and is the scale the tensor core
+ * applies itself. (The pages name FP8 for core tokens and low-precision caches without a recipe.)
+ * The calls below take a nullable device precision flag `prec`: with *prec == SB_SKIP (a module the
+ * TDC skips) they write nothing. */
+
+/* FP8 matrix: blocks of 128 consecutive channels of a row (the last block of a row may be 64). */
+typedef struct {
+  uint8_t* codes;   /* [rows][cols] E4M3 */
+  uint8_t* sf;      /* sb_fp8_sf_bytes(rows, cols) bytes: 512-byte atoms of 128 rows x 4 blocks, atom
+                     * (r / 128) * ceil(cols / 512) + c / 512, byte (r % 32) * 16 + (r % 128) / 32 * 4
+                     * + c / 128 % 4 inside it; zero for rows and blocks past the end */
+  int64_t rows, cols;
+} sb_fp8;
+
+/* A linear layer prepared for sb_linear_fp8. */
+typedef struct {
+  const void* bias_bf16;  /* [N] bf16 or NULL */
+  sb_fp8 w;               /* [N][K] */
+  int64_t N, K;
+} sb_weight_fp8;
+
+/* Bytes of the scale array of an FP8 matrix: ceil(rows/128) * ceil(cols/512) * 512. */
+int64_t sb_fp8_sf_bytes(int64_t rows, int64_t cols);
+
+/* Codes and scales of X [M][K] bf16. K % 64 == 0, K <= 16384 (SB_EUNSUPPORTED). An Inf or NaN in X
+ * is reported as SB_ENONFINITE by sb_check (Inf is coded as +-448, NaN as 0x7f). */
+sb_status sb_fp8_encode(const void* X, int64_t M, int64_t K, const int32_t* prec, const sb_fp8* a /* host */,
+                        void* ws, sb_stream stream);
+
+/* Offline weight preparation: the FP8 copy of W [N][K] bf16 (N % 32 == 0) into w->w, whose buffers
+ * the caller provides; fills the other fields of w. The bf16 W is not read afterwards. */
+sb_status sb_prepare_weight_fp8(const void* W, const void* bias, int64_t N, int64_t K,
+                                sb_weight_fp8* w /* host */, void* ws, sb_stream stream);
+
+/* Y [M][N] = act(X W^T + bias) with both operands in FP8 and FP32 accumulation. With X given (bf16
+ * [M][K]) the call encodes X into `a` first, as sb_fp8_encode does; with X NULL it multiplies the
+ * codes that `a` holds (one encode then serves several layers). epilogue SB_EPI_NONE or
+ * SB_EPI_GELU_TANH; out_dtype SB_OUT_BF16 or SB_OUT_F32; M in [1, 2^30]. Y must not overlap X, `a`
+ * or the weight. */
+sb_status sb_linear_fp8(const void* X, const sb_fp8* a /* host */, const int32_t* prec,
+                        const sb_weight_fp8* w /* host */, int32_t epilogue, int32_t out_dtype, void* Y, int64_t M,
+                        void* ws, sb_stream stream);
+
+/* ---- Attention over an FP8 key/value cache --------------------------------------------------------
+ * The step between the q/k/v projections and the output projection of an attention module. The cache
+ * holds the keys and values of up to `capacity` tokens for each of `batch` sequences, in FP8 with one
+ * E8M0 scale for each block of 64 consecutive positions of one head. */
+typedef struct {
+  uint8_t* k_codes;  /* [batch][heads][capacity][dim] E4M3 */
+  uint8_t* v_codes;  /* [batch][heads][capacity][dim] E4M3 */
+  uint8_t* k_exp;    /* [batch][heads][capacity / 64] E8M0 */
+  uint8_t* v_exp;    /* [batch][heads][capacity / 64] E8M0 */
+  int32_t* lens;     /* [batch] tokens held, in [0, capacity]; the caller may lower it to drop tokens */
+  int64_t batch, heads, capacity; /* capacity % 64 == 0, <= 2^30; batch, heads <= 16384, batch * heads <= 2^20 */
+  int32_t dim;                    /* 64 or 128 */
+} sb_kv8;
+
+/* Bytes of workspace for sb_kv8_attention calls with at most these sizes (any number of key heads);
+ * sb_kv8_store needs 256. Zero it with sb_workspace_init before its first use. */
+sb_status sb_kv8_workspace_size(int64_t batch, int64_t heads_q, int64_t n_q, int32_t dim, size_t* bytes /* host */);
+
+/* Write the keys and values of new tokens into the cache. k, v: bf16, element (b, t, h, c) at
+ * b * strides[0] + t * strides[1] + h * strides[2] + c (host arrays of element strides, each a
+ * multiple of 8 and >= 0), t < n. Sequence b's tokens go to positions start[b] .. start[b] +
+ * counts[b] - 1 (device int32; start NULL: lens[b], counts NULL: n), over tokens held there before,
+ * and lens[b] becomes start[b] + counts[b]. A block whose first position is among the new tokens takes
+ * its exponent from the new tokens in it; a block that holds earlier tokens in front of start[b] keeps
+ * its exponent unless the new tokens need a larger one, and then its earlier codes are rounded to the
+ * larger one. A sequence with start outside [0, lens[b]], counts outside [0, n] or an end past the
+ * capacity is left as it is and SB_ESHAPE is reported by sb_check; an Inf or NaN gives SB_ENONFINITE. */
+sb_status sb_kv8_store(const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides, int64_t n,
+                       const sb_kv8* cache /* host */, const int32_t* start, const int32_t* counts,
+                       const int32_t* prec, void* ws, sb_stream stream);
+
+typedef struct {
+  float scale;     /* factor of q . k before the softmax, > 0 and finite */
+  int32_t causal;  /* 0: every query stands at the last token held; 1: query i of n at len - n + i */
+  int64_t window;  /* > 0: only the last `window` positions up to the query's, and ... */
+  int64_t sinks;   /* ... the first `sinks` positions are visible; 0 with window 0 */
+} sb_attn;
+
+/* out = softmax(scale * q k^T) v over the tokens that the cache holds. q, out: bf16, strides as for
+ * sb_kv8_store (outputs must not overlap one another); heads_q is a multiple of cache->heads, query head
+ * h reads key head h / (heads_q / heads). q_lens (device int32 [batch], NULL: n_q): the sequence's
+ * queries are its first q_lens[b] rows; the rows behind them are left as they are in out and lse.
+ * A query at position p sees key j iff j < lens[b], j <= p and (window == 0 or p - j < window or
+ * j < sinks). A query that sees no key gives zeros and lse -inf. lse (nullable): FP32
+ * [batch][heads_q][n_q], the natural log of the sum of exp(scale * q . k). Keys and values enter the
+ * products exactly; softmax weights are rounded to fp16 for the second product, all sums are FP32.
+ * lens or q_lens out of range are clamped and SB_ESHAPE is reported by sb_check. ws_bytes: size of ws
+ * (SB_ESHAPE if too small). */
+sb_status sb_kv8_attention(const void* q, const int64_t* q_strides, int64_t n_q, int64_t heads_q,
+                           const sb_kv8* cache /* host */, const sb_attn* opt /* host */, const int32_t* q_lens,
+                           void* out, const int64_t* out_strides, float* lse, const int32_t* prec, void* ws,
+                           size_t ws_bytes, sb_stream stream);
+
 /* Bounded device-side wait, the library's failure-detection primitive (the pages have no
  * counterpart). Enqueues on `stream` a one-thread kernel that polls the device int32 at `flag`
  * (acquire loads, ~1 us apart) until it equals `value`. If `limit_ns` nanoseconds of device time
@@ -470,7 +570,8 @@ sb_status sb_wait_flag(const int32_t* flag, int32_t value, uint64_t limit_ns, vo
 sb_status sb_drill_gemm_stall(int64_t withhold_stage, uint64_t limit_ns);
 
 /* Synchronise `stream`, read and clear the device error word of `ws`. Returns SB_OK,
- * SB_ETIMEOUT, SB_ENONFINITE, SB_EINVAL or SB_ECUDA. */
+ * SB_ETIMEOUT, SB_ENONFINITE, SB_ESHAPE (a length on the device out of range), SB_EINVAL or
+ * SB_ECUDA. */
 sb_status sb_check(void* ws, sb_stream stream);
 
 #ifdef __cplusplus

@@ -887,6 +887,214 @@ sb_status sb_delta_combine(const float* y_delta, const float* y_core, int64_t M,
   return ok();
 }
 
+// ---- 8-bit floating point: linear layer, key/value cache, attention ----
+
+int64_t sb_fp8_sf_bytes(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0) return -1;
+  return sb::ceil_div(rows, 128) * sb::ceil_div(cols, 512) * 512;
+}
+
+static sb_status check_fp8(const sb_fp8* t, int64_t rows, int64_t cols, const char* name) {
+  SB_REQUIRE(t->codes && t->sf, SB_EINVAL, "%s: codes and sf are required", name);
+  SB_ALIGNED(t->codes, name);
+  SB_ALIGNED(t->sf, name);
+  SB_REQUIRE(t->rows == rows && t->cols == cols, SB_ESHAPE, "%s is [%lld x %lld], expected [%lld x %lld]", name,
+             (long long)t->rows, (long long)t->cols, (long long)rows, (long long)cols);
+  return SB_OK;
+}
+
+static sb_status check_prec(const int32_t* prec) {
+  SB_REQUIRE((reinterpret_cast<uintptr_t>(prec) & 3u) == 0, SB_EALIGN, "prec misaligned");
+  return SB_OK;
+}
+
+static sb_status check_fp8_shape(int64_t M, int64_t K) {
+  SB_REQUIRE(M >= 1 && M <= (int64_t)1 << 30, SB_ESHAPE, "rows must be in [1, 2^30] (got %lld)", (long long)M);
+  SB_REQUIRE(K >= 64 && K % 64 == 0 && K <= sb::kMaxK, SB_EUNSUPPORTED,
+             "K must be a positive multiple of 64 up to %d (got %lld)", sb::kMaxK, (long long)K);
+  return SB_OK;
+}
+
+sb_status sb_fp8_encode(const void* X, int64_t M, int64_t K, const int32_t* prec, const sb_fp8* a, void* ws,
+                        sb_stream stream) {
+  SB_REQUIRE(X && a && ws, SB_EINVAL, "X, a and ws are required");
+  SB_ALIGNED(X, "X");
+  SB_ALIGNED(ws, "ws");
+  sb_status st = check_fp8_shape(M, K);
+  if (st != SB_OK || (st = check_fp8(a, M, K, "a")) != SB_OK || (st = check_prec(prec)) != SB_OK) return st;
+  cudaError_t e = sb::launch_fp8_encode(X, M, K, prec, a->codes, a->sf, ws, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "sb_fp8_encode");
+  return ok();
+}
+
+sb_status sb_prepare_weight_fp8(const void* W, const void* bias, int64_t N, int64_t K, sb_weight_fp8* w, void* ws,
+                                sb_stream stream) {
+  SB_REQUIRE(W && w && ws, SB_EINVAL, "W, w and ws are required");
+  SB_ALIGNED(W, "W");
+  SB_ALIGNED(ws, "ws");
+  if (bias) SB_ALIGNED(bias, "bias");
+  sb_status st = check_fp8_shape(N, K);
+  if (st != SB_OK) return st;
+  SB_REQUIRE(N % 32 == 0, SB_EUNSUPPORTED, "N must be a multiple of 32 (got %lld)", (long long)N);
+  if ((st = check_fp8(&w->w, N, K, "w->w")) != SB_OK) return st;
+  w->bias_bf16 = bias;
+  w->N = N;
+  w->K = K;
+  cudaError_t e = sb::launch_fp8_encode(W, N, K, nullptr, w->w.codes, w->w.sf, ws, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "sb_prepare_weight_fp8");
+  return ok();
+}
+
+sb_status sb_linear_fp8(const void* X, const sb_fp8* a, const int32_t* prec, const sb_weight_fp8* w, int32_t epilogue,
+                        int32_t out_dtype, void* Y, int64_t M, void* ws, sb_stream stream) {
+  SB_REQUIRE(a && w && Y && ws, SB_EINVAL, "a, w, Y and ws are required");
+  if (X) SB_ALIGNED(X, "X");
+  SB_ALIGNED(Y, "Y");
+  SB_ALIGNED(ws, "ws");
+  if (w->bias_bf16) SB_ALIGNED(w->bias_bf16, "bias");
+  SB_REQUIRE(epilogue == SB_EPI_NONE || epilogue == SB_EPI_GELU_TANH, SB_EINVAL, "unknown epilogue %d", (int)epilogue);
+  SB_REQUIRE(out_dtype == SB_OUT_BF16 || out_dtype == SB_OUT_F32, SB_EINVAL, "out_dtype must be BF16 or F32 (got %d)",
+             (int)out_dtype);
+  sb_status st = check_fp8_shape(M, w->K);
+  if (st != SB_OK) return st;
+  SB_REQUIRE(w->N >= 32 && w->N % 32 == 0 && w->N <= (int64_t)1 << 30, SB_EUNSUPPORTED,
+             "N must be a positive multiple of 32 (got %lld)", (long long)w->N);
+  if ((st = check_fp8(&w->w, w->N, w->K, "w->w")) != SB_OK || (st = check_fp8(a, M, w->K, "a")) != SB_OK ||
+      (st = check_prec(prec)) != SB_OK)
+    return st;
+  sb::Fp8Linear p{};
+  p.M = M;
+  p.N = w->N;
+  p.K = w->K;
+  p.X = X;
+  p.A = a->codes;
+  p.sfA = a->sf;
+  p.W = w->w.codes;
+  p.sfW = w->w.sf;
+  p.bias = w->bias_bf16;
+  p.prec = prec;
+  p.epilogue = epilogue;
+  p.out_dtype = out_dtype;
+  p.Y = Y;
+  p.hdr = ws;
+  const char* why = "";
+  cudaError_t e = sb::launch_fp8_linear(p, (cudaStream_t)stream, &why);
+  if (e != cudaSuccess) return cuda_fail(e, why);
+  return ok();
+}
+
+static sb_status check_kv8(const sb_kv8* c) {
+  SB_REQUIRE(c->k_codes && c->v_codes && c->k_exp && c->v_exp && c->lens, SB_EINVAL,
+             "cache: k_codes, v_codes, k_exp, v_exp and lens are required");
+  SB_ALIGNED(c->k_codes, "cache->k_codes");
+  SB_ALIGNED(c->v_codes, "cache->v_codes");
+  SB_ALIGNED(c->k_exp, "cache->k_exp");
+  SB_ALIGNED(c->v_exp, "cache->v_exp");
+  SB_ALIGNED(c->lens, "cache->lens");
+  SB_REQUIRE(c->dim == 64 || c->dim == 128, SB_EUNSUPPORTED, "cache->dim must be 64 or 128 (got %d)", (int)c->dim);
+  SB_REQUIRE(c->batch >= 1 && c->batch <= 16384 && c->heads >= 1 && c->heads <= 16384 &&
+                 c->batch * c->heads <= (int64_t)1 << 20,
+             SB_ESHAPE, "cache: batch and heads must be in [1, 16384], their product at most 2^20");
+  SB_REQUIRE(c->capacity >= 64 && c->capacity <= (int64_t)1 << 30 && c->capacity % 64 == 0, SB_ESHAPE,
+             "cache->capacity must be a multiple of 64 in [64, 2^30] (got %lld)", (long long)c->capacity);
+  return SB_OK;
+}
+
+static sb_status check_strides(const int64_t* s, int64_t tokens, int64_t heads, int64_t batch, const char* name) {
+  const int64_t count[3] = {batch, tokens, heads};
+  for (int i = 0; i < 3; ++i) {
+    SB_REQUIRE(s[i] >= 0 && s[i] % 8 == 0, SB_EALIGN, "%s: strides must be multiples of 8 elements, not negative", name);
+    SB_REQUIRE(s[i] <= ((int64_t)1 << 55) / count[i], SB_ESHAPE, "%s: strides too large", name);
+  }
+  return SB_OK;
+}
+
+sb_status sb_kv8_workspace_size(int64_t batch, int64_t heads_q, int64_t n_q, int32_t dim, size_t* bytes) {
+  SB_REQUIRE(bytes != nullptr, SB_EINVAL, "bytes is NULL");
+  SB_REQUIRE(batch >= 1 && batch <= 16384 && heads_q >= 1 && heads_q <= 16384 && n_q >= 1 &&
+                 n_q <= (int64_t)1 << 30,
+             SB_ESHAPE, "batch and heads_q must be in [1, 16384], n_q in [1, 2^30]");
+  SB_REQUIRE(dim == 64 || dim == 128, SB_EUNSUPPORTED, "dim must be 64 or 128 (got %d)", (int)dim);
+  *bytes = sb::kv8_workspace_bytes(batch, heads_q, n_q, dim);
+  return ok();
+}
+
+sb_status sb_kv8_store(const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides, int64_t n,
+                       const sb_kv8* cache, const int32_t* start, const int32_t* counts, const int32_t* prec, void* ws,
+                       sb_stream stream) {
+  SB_REQUIRE(k && v && k_strides && v_strides && cache && ws, SB_EINVAL,
+             "k, v, their strides, cache and ws are required");
+  SB_ALIGNED(k, "k");
+  SB_ALIGNED(v, "v");
+  SB_ALIGNED(ws, "ws");
+  sb_status st = check_kv8(cache);
+  if (st != SB_OK) return st;
+  SB_REQUIRE(n >= 1 && n <= cache->capacity, SB_ESHAPE, "n must be in [1, capacity] (got %lld)", (long long)n);
+  if ((st = check_strides(k_strides, n, cache->heads, cache->batch, "k")) != SB_OK ||
+      (st = check_strides(v_strides, n, cache->heads, cache->batch, "v")) != SB_OK || (st = check_prec(prec)) != SB_OK)
+    return st;
+  SB_REQUIRE((reinterpret_cast<uintptr_t>(start) & 3u) == 0 && (reinterpret_cast<uintptr_t>(counts) & 3u) == 0,
+             SB_EALIGN, "start or counts misaligned");
+  sb::Kv8Store p{};
+  p.c = *cache;
+  p.k = k;
+  p.v = v;
+  for (int i = 0; i < 3; ++i) p.ks[i] = k_strides[i], p.vs[i] = v_strides[i];
+  p.n = n;
+  p.start = start;
+  p.counts = counts;
+  p.prec = prec;
+  p.hdr = static_cast<sb::WsHeader*>(ws);
+  cudaError_t e = sb::launch_kv8_store(p, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "sb_kv8_store");
+  return ok();
+}
+
+sb_status sb_kv8_attention(const void* q, const int64_t* q_strides, int64_t n_q, int64_t heads_q, const sb_kv8* cache,
+                           const sb_attn* opt, const int32_t* q_lens, void* out, const int64_t* out_strides, float* lse,
+                           const int32_t* prec, void* ws, size_t ws_bytes, sb_stream stream) {
+  SB_REQUIRE(q && q_strides && cache && opt && out && out_strides && ws, SB_EINVAL,
+             "q, out, their strides, cache, opt and ws are required");
+  SB_ALIGNED(q, "q");
+  SB_ALIGNED(out, "out");
+  SB_ALIGNED(ws, "ws");
+  if (lse) SB_ALIGNED(lse, "lse");
+  sb_status st = check_kv8(cache);
+  if (st != SB_OK) return st;
+  SB_REQUIRE(heads_q >= 1 && heads_q <= 16384 && heads_q % cache->heads == 0, SB_ESHAPE,
+             "heads_q (%lld) must be a multiple of the cache's heads (%lld)", (long long)heads_q,
+             (long long)cache->heads);
+  SB_REQUIRE(n_q >= 1 && n_q <= (int64_t)1 << 30, SB_ESHAPE, "n_q must be in [1, 2^30] (got %lld)", (long long)n_q);
+  SB_REQUIRE(opt->scale > 0.0f && opt->scale <= 3.4e38f, SB_EINVAL, "scale must be positive and finite");
+  SB_REQUIRE(opt->window >= 0 && opt->sinks >= 0 && (opt->window > 0 || opt->sinks == 0), SB_EINVAL,
+             "window and sinks must not be negative, and sinks need a window");
+  if ((st = check_strides(q_strides, n_q, heads_q, cache->batch, "q")) != SB_OK ||
+      (st = check_strides(out_strides, n_q, heads_q, cache->batch, "out")) != SB_OK || (st = check_prec(prec)) != SB_OK)
+    return st;
+  SB_REQUIRE((reinterpret_cast<uintptr_t>(q_lens) & 3u) == 0, SB_EALIGN, "q_lens misaligned");
+  const size_t need = sb::kv8_workspace_bytes(cache->batch, heads_q, n_q, cache->dim);
+  SB_REQUIRE(ws_bytes >= need, SB_ESHAPE, "ws holds %zu bytes, %zu are needed", ws_bytes, need);
+  sb::Kv8Attn p{};
+  p.c = *cache;
+  p.q = q;
+  p.out = out;
+  for (int i = 0; i < 3; ++i) p.qs[i] = q_strides[i], p.os[i] = out_strides[i];
+  p.n_q = n_q;
+  p.heads_q = heads_q;
+  p.scale = opt->scale;
+  p.causal = opt->causal ? 1 : 0;
+  p.window = opt->window;
+  p.sinks = opt->sinks;
+  p.q_lens = q_lens;
+  p.lse = lse;
+  p.prec = prec;
+  p.hdr = static_cast<sb::WsHeader*>(ws);
+  const char* why = "";
+  cudaError_t e = sb::launch_kv8_attention(p, (cudaStream_t)stream, &why);
+  if (e != cudaSuccess) return cuda_fail(e, why);
+  return ok();
+}
+
 sb_status sb_check(void* ws, sb_stream stream) {
   SB_REQUIRE(ws != nullptr, SB_EINVAL, "ws is NULL");
   cudaStream_t s = (cudaStream_t)stream;

@@ -39,7 +39,7 @@ struct WsHeader {
 };
 static_assert(sizeof(WsHeader) == 128, "WsHeader layout");
 
-enum { TICKET_PREPASS = 0, TICKET_TDC = 1 };
+enum { TICKET_PREPASS = 0, TICKET_TDC = 1, TICKET_KV = 2 };
 
 constexpr int kGroupRows = 16;  // rows per FP64 group partial
 constexpr int kMaxK = 16384;

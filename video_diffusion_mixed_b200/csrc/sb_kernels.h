@@ -9,6 +9,8 @@
 
 namespace sb {
 
+struct WsHeader;
+
 struct PrepassLaunch {
   const void* X;
   const void* R;
@@ -178,6 +180,55 @@ cudaError_t launch_delta_split(const void* X, int64_t K, const DeltaCubes& c, in
                                float* scale, void* core16, void* delta, cudaStream_t s);
 cudaError_t launch_delta_combine(const float* Yd, const float* Yc, int64_t M, int64_t N, const DeltaCubes& c,
                                  int gelu, void* Y, cudaStream_t s);
+
+// FP8 linear layer (fp8.cu): A and W with their tiled E8M0 scales.
+struct Fp8Linear {
+  int64_t M, N, K;
+  const void* X;  // bf16 rows to encode into A first, or null
+  uint8_t* A;
+  uint8_t* sfA;
+  const uint8_t* W;
+  const uint8_t* sfW;
+  const void* bias;
+  const int32_t* prec;
+  int epilogue;
+  int out_dtype;
+  void* Y;
+  void* hdr;
+};
+cudaError_t launch_fp8_encode(const void* X, int64_t M, int64_t K, const int32_t* prec, uint8_t* codes, uint8_t* sf,
+                              void* hdr, cudaStream_t s);
+cudaError_t launch_fp8_linear(const Fp8Linear& p, cudaStream_t s, const char** why);
+
+// FP8 key/value cache (kv8.cu). Strides are in elements: sequence, token, head.
+struct Kv8Store {
+  sb_kv8 c;
+  const void* k;
+  const void* v;
+  int64_t ks[3], vs[3];
+  int64_t n;
+  const int32_t* start;
+  const int32_t* counts;
+  const int32_t* prec;
+  WsHeader* hdr;
+};
+struct Kv8Attn {
+  sb_kv8 c;
+  const void* q;
+  void* out;
+  int64_t qs[3], os[3];
+  int64_t n_q, heads_q;
+  float scale;
+  int causal;
+  int64_t window, sinks;
+  const int32_t* q_lens;
+  float* lse;
+  const int32_t* prec;
+  WsHeader* hdr;
+};
+cudaError_t launch_kv8_store(const Kv8Store& p, cudaStream_t s);
+cudaError_t launch_kv8_attention(const Kv8Attn& p, cudaStream_t s, const char** why);
+size_t kv8_workspace_bytes(int64_t batch, int64_t heads_q, int64_t n_q, int dim);
 
 sb_status report_error(sb_status st, const char* msg);
 

@@ -63,6 +63,26 @@ class Cubes(ctypes.Structure):
                 ("width", ctypes.c_int64), ("ct", ctypes.c_int32), ("ch", ctypes.c_int32), ("cw", ctypes.c_int32)]
 
 
+class Fp8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("sf", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64)]
+
+
+class WeightFp8C(ctypes.Structure):
+    _fields_ = [("bias_bf16", ctypes.c_void_p), ("w", Fp8), ("N", ctypes.c_int64), ("K", ctypes.c_int64)]
+
+
+class Kv8(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("batch", ctypes.c_int64),
+                ("heads", ctypes.c_int64), ("capacity", ctypes.c_int64), ("dim", ctypes.c_int32)]
+
+
+class Attn(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("causal", ctypes.c_int32), ("window", ctypes.c_int64),
+                ("sinks", ctypes.c_int64)]
+
+
 STATE_BYTES = 64
 STATS_BYTES = 96
 STATE_FIELDS = ("prev_d", "acc", "delta", "have_d", "n_out", "last_skipped", "skip", "steps")
@@ -119,6 +139,13 @@ def lib():
             "sb_cube_count": (i64, [P(Cubes), i64]),
             "sb_delta_split": (st, [vp, i64, i64, P(Cubes), vp, vp, vp, vp, vp]),
             "sb_delta_combine": (st, [vp, vp, i64, i64, P(Cubes), i32, vp, vp]),
+            "sb_fp8_sf_bytes": (i64, [i64, i64]),
+            "sb_fp8_encode": (st, [vp, i64, i64, vp, P(Fp8), vp, vp]),
+            "sb_prepare_weight_fp8": (st, [vp, vp, i64, i64, P(WeightFp8C), vp, vp]),
+            "sb_linear_fp8": (st, [vp, P(Fp8), vp, P(WeightFp8C), i32, i32, vp, i64, vp, vp]),
+            "sb_kv8_workspace_size": (st, [i64, i64, i64, i32, P(ctypes.c_size_t)]),
+            "sb_kv8_store": (st, [vp, vp, vp, vp, i64, P(Kv8), vp, vp, vp, vp, vp]),
+            "sb_kv8_attention": (st, [vp, vp, i64, i64, P(Kv8), P(Attn), vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -135,7 +162,8 @@ EXPORTED = ("sb_version", "sb_last_error", "sb_workspace_size", "sb_workspace_in
             "sb_tdc_record_partial", "sb_tdc_finish", "sb_module_decide", "sb_prepass_chunks", "sb_cube_count",
             "sb_delta_split", "sb_delta_combine", "sb_drill_gemm_stall", "sb_tdc_refresh_fp8",
             "sb_tdc_reuse_fp8", "sb_module_record", "sb_delta_linear", "sb_linear_records",
-            "sb_chunk_records", "sb_linear_module_record")
+            "sb_chunk_records", "sb_linear_module_record", "sb_fp8_sf_bytes", "sb_fp8_encode",
+            "sb_prepare_weight_fp8", "sb_linear_fp8", "sb_kv8_workspace_size", "sb_kv8_store", "sb_kv8_attention")
 
 
 def _ck(status: int):
@@ -496,3 +524,178 @@ def delta_linear(delta, a4, a8, prec, w: "Weight", y_core, c: Cubes, Y, epilogue
 def delta_combine(y_delta, y_core, c: Cubes, Y, epilogue: int = EPI_NONE, stream=None):
     M, N = Y.shape
     _ck(lib().sb_delta_combine(_p(y_delta), _p(y_core), M, N, ctypes.byref(c), epilogue, _p(Y), _stream(stream)))
+
+
+# ---- 8-bit floating point (include/sixbit.h): linear layer, key/value cache, attention ----
+
+def _need(cond: bool, status: int, msg: str):
+    if not cond:
+        raise SixbitError(status, msg)
+
+
+def _dev(device, *tensors):
+    """The tensors are CUDA tensors of one device, and it is the current one (kernels launch there)."""
+    for t in tensors:
+        if t is not None:
+            _need(t.is_cuda, SB_EINVAL, "a tensor is not on a CUDA device")
+            _need(t.device == device, SB_EINVAL, f"a tensor is on {t.device}, another on {device}")
+    _need(device.index == torch.cuda.current_device(), SB_EINVAL,
+          f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _typed(t, dtype, shape, name: str):
+    if t is not None:
+        _need(t.dtype == dtype, SB_EINVAL, f"{name} must be {dtype}, not {t.dtype}")
+        _need(tuple(t.shape) == tuple(shape), SB_ESHAPE, f"{name} is {tuple(t.shape)}, expected {tuple(shape)}")
+        _need(t.is_contiguous(), SB_EINVAL, f"{name} must be contiguous")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+class Fp8Tensor:
+    """Caller-owned FP8 matrix (sb_fp8): E4M3 codes and E8M0 scales of blocks of 128 channels."""
+
+    def __init__(self, rows: int, cols: int, device="cuda"):
+        self.rows, self.cols = rows, cols
+        self.codes = torch.empty((rows, cols), dtype=torch.uint8, device=device)
+        self.sf = torch.empty(int(lib().sb_fp8_sf_bytes(rows, cols)), dtype=torch.uint8, device=device)
+        self._c = Fp8(self.codes.data_ptr(), self.sf.data_ptr(), rows, cols)
+
+    def c(self) -> Fp8:
+        return self._c
+
+    def exponents(self) -> torch.Tensor:
+        """The scale bytes as [rows, ceil(cols / 128)], out of their tiled layout."""
+        nb, groups = -(-self.cols // 128), -(-self.cols // 512)
+        t = self.sf.view(-1, groups, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(-1, groups * 4)
+        return t[:self.rows, :nb].contiguous()
+
+
+class WeightFp8:
+    """A linear layer prepared for linear_fp8: the FP8 copy of W [N, K] and the bf16 bias."""
+
+    def __init__(self, W: torch.Tensor, bias: torch.Tensor | None = None, ws: Workspace | None = None, stream=None):
+        N, K = W.shape
+        _dev(W.device, W, bias)
+        _typed(W, torch.bfloat16, (N, K), "W")
+        _typed(bias, torch.bfloat16, (N,), "bias")
+        self.N, self.K, self.bias = N, K, bias
+        self.w = Fp8Tensor(N, K, W.device)
+        self._c = WeightFp8C()
+        self._c.w = self.w.c()
+        ws = ws or Workspace(1, 1, W.device, stream)
+        _ck(lib().sb_prepare_weight_fp8(_ptr(W), _ptr(bias), N, K, ctypes.byref(self._c), ws.ptr, _stream(stream)))
+
+    def c(self) -> WeightFp8C:
+        return self._c
+
+
+def fp8_encode(X, a: Fp8Tensor, ws: Workspace, prec=None, stream=None):
+    """sb_fp8_encode: the codes and scales of X [M, K] bf16 into a."""
+    M, K = X.shape
+    _dev(X.device, X, a.codes, prec)
+    _typed(X, torch.bfloat16, (M, K), "X")
+    _ck(lib().sb_fp8_encode(_ptr(X), M, K, _ptr(prec), ctypes.byref(a.c()), ws.ptr, _stream(stream)))
+
+
+def linear_fp8(X, a: Fp8Tensor, w: WeightFp8, Y, epilogue: int = EPI_NONE, prec=None, ws: Workspace = None,
+               stream=None):
+    """sb_linear_fp8: Y = act(X W^T + bias) in FP8; X None multiplies the codes that a holds. The
+    output type is Y's (bf16 or float32)."""
+    M = a.rows
+    _need(ws is not None, SB_EINVAL, "ws is required")
+    _dev(Y.device, Y, X, a.codes, w.w.codes, prec)
+    _typed(X, torch.bfloat16, (M, w.K), "X")
+    _need(Y.dtype in (torch.bfloat16, torch.float32), SB_EINVAL, f"Y must be bfloat16 or float32, not {Y.dtype}")
+    _typed(Y, Y.dtype, (M, w.N), "Y")
+    out = OUT_F32 if Y.dtype == torch.float32 else OUT_BF16
+    _ck(lib().sb_linear_fp8(_ptr(X), ctypes.byref(a.c()), _ptr(prec), ctypes.byref(w.c()), epilogue, out, _ptr(Y), M,
+                            ws.ptr, _stream(stream)))
+
+
+class KvCache8:
+    """Caller-owned FP8 key/value cache (sb_kv8) of `batch` sequences, `heads` heads of `dim` channels
+    and `capacity` tokens. buffers: existing (k_codes, k_exp, v_codes, v_exp, lens) to use instead of
+    new ones; new ones hold no tokens."""
+
+    def __init__(self, batch: int, heads: int, capacity: int, dim: int, device="cuda", buffers=None):
+        self.batch, self.heads, self.capacity, self.dim = batch, heads, capacity, dim
+        if buffers is None:
+            def new(*shape):
+                return torch.zeros(shape, dtype=torch.uint8, device=device)
+            buffers = (new(batch, heads, capacity, dim), new(batch, heads, capacity // 64),
+                       new(batch, heads, capacity, dim), new(batch, heads, capacity // 64),
+                       torch.zeros(batch, dtype=torch.int32, device=device))
+        self.k_codes, self.k_exp, self.v_codes, self.v_exp, self.lens = buffers
+        for t, name in ((self.k_codes, "k_codes"), (self.v_codes, "v_codes")):
+            _typed(t, torch.uint8, (batch, heads, capacity, dim), name)
+        for t, name in ((self.k_exp, "k_exp"), (self.v_exp, "v_exp")):
+            _typed(t, torch.uint8, (batch, heads, capacity // 64), name)
+        _typed(self.lens, torch.int32, (batch,), "lens")
+        self.device = self.k_codes.device
+        for t in buffers:
+            _need(t.is_cuda and t.device == self.device, SB_EINVAL, "the cache's buffers must be on one CUDA device")
+        self._c = Kv8(self.k_codes.data_ptr(), self.v_codes.data_ptr(), self.k_exp.data_ptr(), self.v_exp.data_ptr(),
+                      self.lens.data_ptr(), batch, heads, capacity, dim)
+
+    def c(self) -> Kv8:
+        return self._c
+
+
+class AttnWorkspace:
+    """Workspace of kv8_attention calls with at most these sizes (and of kv8_store and linear_fp8)."""
+
+    def __init__(self, batch: int, heads_q: int, n_q: int, dim: int, device="cuda", stream=None):
+        n = ctypes.c_size_t(0)
+        _ck(lib().sb_kv8_workspace_size(batch, heads_q, n_q, dim, ctypes.byref(n)))
+        self.bytes = n.value
+        self.buf = torch.empty(self.bytes, dtype=torch.uint8, device=device)
+        _ck(lib().sb_workspace_init(_p(self.buf), self.bytes, _stream(stream)))
+
+    @property
+    def ptr(self):
+        return _p(self.buf)
+
+
+def _strides(t, name: str):
+    """(batch, token, head) strides of a [B, T, H, D] bf16 tensor whose channels are contiguous (0 for
+    an axis of one)."""
+    _need(t.dtype == torch.bfloat16, SB_EINVAL, f"{name} must be torch.bfloat16, not {t.dtype}")
+    _need(t.stride(3) == 1, SB_EINVAL, f"{name}: the channels of a head must be contiguous")
+    return (ctypes.c_int64 * 3)(*(0 if n == 1 else s for n, s in zip(t.shape[:3], t.stride())))
+
+
+def kv8_store(k, v, cache: KvCache8, start=None, counts=None, prec=None, ws=None, stream=None):
+    """sb_kv8_store: keys and values [B, n, H, D] bf16 (any strides with contiguous channels) into the
+    cache at positions start[b] (None: behind the tokens held); counts[b] of the n rows (None: all)."""
+    n = k.shape[1]
+    _need(ws is not None, SB_EINVAL, "ws is required")
+    _dev(cache.device, k, v, start, counts, prec)
+    for t, name in ((k, "k"), (v, "v")):
+        _need(tuple(t.shape) == (cache.batch, n, cache.heads, cache.dim), SB_ESHAPE,
+              f"{name} is {tuple(t.shape)}, expected {(cache.batch, n, cache.heads, cache.dim)}")
+    _typed(start, torch.int32, (cache.batch,), "start")
+    _typed(counts, torch.int32, (cache.batch,), "counts")
+    _ck(lib().sb_kv8_store(_ptr(k), _strides(k, "k"), _ptr(v), _strides(v, "v"), n, ctypes.byref(cache.c()),
+                           _ptr(start), _ptr(counts), _ptr(prec), ws.ptr, _stream(stream)))
+
+
+def kv8_attention(q, cache: KvCache8, out, lse=None, scale: float | None = None, causal: bool = False,
+                  window: int = 0, sinks: int = 0, q_lens=None, prec=None, ws: AttnWorkspace = None, stream=None):
+    """sb_kv8_attention: out [B, n, Hq, D] = softmax(scale q k^T) v over the cache; scale None is
+    1 / sqrt(D); lse: float32 [B, Hq, n] or None."""
+    B, n, Hq, D = q.shape
+    _need(ws is not None, SB_EINVAL, "ws is required")
+    _dev(cache.device, q, out, lse, q_lens, prec)
+    _need((B, D) == (cache.batch, cache.dim), SB_ESHAPE, f"q is {tuple(q.shape)}, the cache holds {cache.batch} "
+          f"sequences of heads of {cache.dim}")
+    _need(out.shape == q.shape, SB_ESHAPE, f"out is {tuple(out.shape)}, expected {tuple(q.shape)}")
+    _need(all(m == 1 or s > 0 for m, s in zip(out.shape, out.stride())), SB_EINVAL, "out must not be broadcast")
+    _typed(lse, torch.float32, (B, Hq, n), "lse")
+    _typed(q_lens, torch.int32, (B,), "q_lens")
+    opt = Attn(1.0 / D ** 0.5 if scale is None else scale, int(causal), window, sinks)
+    _ck(lib().sb_kv8_attention(_ptr(q), _strides(q, "q"), n, Hq, ctypes.byref(cache.c()), ctypes.byref(opt),
+                               _ptr(q_lens), _ptr(out), _strides(out, "out"), _ptr(lse), _ptr(prec), ws.ptr,
+                               ws.bytes, _stream(stream)))
