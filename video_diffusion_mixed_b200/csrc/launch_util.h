@@ -28,6 +28,26 @@ inline int device_sm_count() {
   return n;
 }
 
+// Launch configuration of a kernel that may start while the launch before it still runs (`early`):
+// the kernel calls griddepcontrol.wait before it touches what that launch writes. Only for a launch
+// that the library itself put in front, which in turn started after everything before it had ended.
+struct LaunchAfter {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  LaunchAfter(unsigned grid, unsigned threads, size_t smem, cudaStream_t s, bool early) {
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
+  }
+  LaunchAfter(const LaunchAfter&) = delete;
+  LaunchAfter& operator=(const LaunchAfter&) = delete;
+};
+
 // Raises the kernel's dynamic shared-memory limit to `bytes` on the current device, once per
 // device (devices 0..63 are remembered; others are set on every call).
 template <class Kernel>

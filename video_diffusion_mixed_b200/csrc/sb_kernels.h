@@ -198,6 +198,7 @@ struct Fp8Linear {
 };
 cudaError_t launch_fp8_encode(const void* X, int64_t M, int64_t K, const int32_t* prec, uint8_t* codes, uint8_t* sf,
                               void* hdr, cudaStream_t s);
+cudaError_t launch_fp8_gemm(const Fp8Linear& p, cudaStream_t s, const char** why);
 cudaError_t launch_fp8_linear(const Fp8Linear& p, cudaStream_t s, const char** why);
 
 // FP8 key/value cache (kv8.cu). Strides are in elements: sequence, token, head.
