@@ -1083,8 +1083,9 @@ sb_status sb_kv8_attention(const void* q, const int64_t* q_strides, int64_t n_q,
   p.heads_q = heads_q;
   p.scale = opt->scale;
   p.causal = opt->causal ? 1 : 0;
-  p.window = opt->window;
-  p.sinks = opt->sinks;
+  const int64_t far = (int64_t)1 << 30;  // positions are below it
+  p.window = opt->window < far ? opt->window : far;
+  p.sinks = opt->sinks < far ? opt->sinks : far;
   p.q_lens = q_lens;
   p.lse = lse;
   p.prec = prec;

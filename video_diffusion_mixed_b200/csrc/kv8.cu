@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(128) k_kv8_attn(Kv8Attn p) {
 }
 
 cudaError_t launch_kv8_attention(const Kv8Attn& p, cudaStream_t s, const char** why) {
+  if (p.n_q * (p.heads_q / p.c.heads) > 16) return launch_kv8_tiles(p, 1, nullptr, s, why);
   *why = "k_kv8_attn launch";
   const dim3 grid((unsigned)ceil_div(p.n_q, 4), (unsigned)p.heads_q, (unsigned)p.c.batch);
   if (p.c.dim == 64)

@@ -229,6 +229,7 @@ struct Kv8Attn {
 };
 cudaError_t launch_kv8_store(const Kv8Store& p, cudaStream_t s);
 cudaError_t launch_kv8_attention(const Kv8Attn& p, cudaStream_t s, const char** why);
+cudaError_t launch_kv8_tiles(const Kv8Attn& p, int splits, float* part, cudaStream_t s, const char** why);
 size_t kv8_workspace_bytes(int64_t batch, int64_t heads_q, int64_t n_q, int dim);
 
 sb_status report_error(sb_status st, const char* msg);
