@@ -507,7 +507,7 @@ typedef struct {
 } sb_kv8;
 
 /* Bytes of workspace for sb_kv8_attention calls with at most these sizes (any number of key heads);
- * sb_kv8_store needs 256. Zero it with sb_workspace_init before its first use. */
+ * sb_kv8_store needs 256; batch * heads_q * n_q at most 2^40. Zero it with sb_workspace_init before its first use. */
 sb_status sb_kv8_workspace_size(int64_t batch, int64_t heads_q, int64_t n_q, int32_t dim, size_t* bytes /* host */);
 
 /* Write the keys and values of new tokens into the cache. k, v: bf16, element (b, t, h, c) at

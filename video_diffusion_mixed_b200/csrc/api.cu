@@ -1014,6 +1014,7 @@ sb_status sb_kv8_workspace_size(int64_t batch, int64_t heads_q, int64_t n_q, int
   SB_REQUIRE(batch >= 1 && batch <= 16384 && heads_q >= 1 && heads_q <= 16384 && n_q >= 1 &&
                  n_q <= (int64_t)1 << 30,
              SB_ESHAPE, "batch and heads_q must be in [1, 16384], n_q in [1, 2^30]");
+  SB_REQUIRE(batch * heads_q * n_q <= (int64_t)1 << 40, SB_ESHAPE, "batch * heads_q * n_q must be at most 2^40");
   SB_REQUIRE(dim == 64 || dim == 128, SB_EUNSUPPORTED, "dim must be 64 or 128 (got %d)", (int)dim);
   *bytes = sb::kv8_workspace_bytes(batch, heads_q, n_q, dim);
   return ok();
@@ -1065,6 +1066,8 @@ sb_status sb_kv8_attention(const void* q, const int64_t* q_strides, int64_t n_q,
              "heads_q (%lld) must be a multiple of the cache's heads (%lld)", (long long)heads_q,
              (long long)cache->heads);
   SB_REQUIRE(n_q >= 1 && n_q <= (int64_t)1 << 30, SB_ESHAPE, "n_q must be in [1, 2^30] (got %lld)", (long long)n_q);
+  SB_REQUIRE(cache->batch * heads_q * n_q <= (int64_t)1 << 40, SB_ESHAPE,
+             "batch * heads_q * n_q must be at most 2^40");
   SB_REQUIRE(opt->scale > 0.0f && opt->scale <= 3.4e38f, SB_EINVAL, "scale must be positive and finite");
   SB_REQUIRE(opt->window >= 0 && opt->sinks >= 0 && (opt->window > 0 || opt->sinks == 0), SB_EINVAL,
              "window and sinks must not be negative, and sinks need a window");
@@ -1091,7 +1094,7 @@ sb_status sb_kv8_attention(const void* q, const int64_t* q_strides, int64_t n_q,
   p.prec = prec;
   p.hdr = static_cast<sb::WsHeader*>(ws);
   const char* why = "";
-  cudaError_t e = sb::launch_kv8_attention(p, (cudaStream_t)stream, &why);
+  cudaError_t e = sb::launch_kv8_attention(p, static_cast<char*>(ws) + sb::kKv8PartOffset, (cudaStream_t)stream, &why);
   if (e != cudaSuccess) return cuda_fail(e, why);
   return ok();
 }

@@ -1,4 +1,4 @@
-// kv8.cu -- FP8 key/value cache: the store of new tokens, and attention over what it holds.
+// kv8.cu -- FP8 key/value cache: the store of new tokens.
 #include "launch_util.h"
 #include "sb_device.cuh"
 #include "sb_kernels.h"
@@ -116,77 +116,6 @@ cudaError_t launch_kv8_store(const Kv8Store& p, cudaStream_t s) {
   const dim3 grid((unsigned)((p.n + 62) / 64 + 1), (unsigned)(2 * p.c.heads), (unsigned)p.c.batch);
   k_kv8_store<<<grid, 128, 0, s>>>(p);
   return cudaGetLastError();
-}
-
-// ------------------------------------------------------------------------------------------------
-// Attention, one warp per query row
-// ------------------------------------------------------------------------------------------------
-
-template <int D>
-__global__ void __launch_bounds__(128) k_kv8_attn(Kv8Attn p) {
-  __shared__ float qs[4][D];
-  if (p.prec && *p.prec == SB_SKIP) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t b = blockIdx.z, hq = blockIdx.y, hk = hq / (p.heads_q / p.c.heads);
-  const int64_t i = (int64_t)blockIdx.x * 4 + warp;
-  int len = p.c.lens[b], nq = p.q_lens ? p.q_lens[b] : (int)p.n_q;
-  if (threadIdx.x == 0 && (len < 0 || len > p.c.capacity || nq < 0 || nq > p.n_q)) set_error(p.hdr, SB_ESHAPE);
-  len = (int)max((int64_t)0, min((int64_t)len, p.c.capacity));
-  nq = (int)max((int64_t)0, min((int64_t)nq, p.n_q));
-  if (i >= nq) return;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + b * p.qs[0] + i * p.qs[1] + hq * p.qs[2];
-  for (int d = lane; d < D; d += 32) qs[warp][d] = __bfloat162float(q[d]);
-  __syncwarp();
-  const int64_t pos = p.causal ? (int64_t)len - nq + i : (int64_t)len - 1;
-  const int64_t end = min((int64_t)len, pos + 1);
-  const int64_t row0 = (b * p.c.heads + hk) * p.c.capacity;
-  const uint8_t* kx = p.c.k_exp + row0 / 64;
-  const uint8_t* vx = p.c.v_exp + row0 / 64;
-  float m = -INFINITY, l = 0.0f, o[D / 32] = {};
-  for (int64_t j0 = 0; j0 < end; j0 += 32) {
-    const int64_t j = j0 + lane;
-    const bool see = j < end && (p.window == 0 || pos - j < p.window || j < p.sinks);
-    if (!__any_sync(0xffffffffu, see)) continue;
-    float s = -INFINITY;
-    if (see) {
-      const uint8_t* kc = p.c.k_codes + (row0 + j) * D;
-      float acc = 0.0f;
-      for (int d = 0; d < D; ++d) acc += qs[warp][d] * e4m3_to_f32(kc[d]);
-      s = acc * kv_pow2(kx[j / 64]) * p.scale;
-    }
-    const float mn = fmaxf(m, warp_max_f32(s));
-    const float f = __expf(m - mn), w = see ? __expf(s - mn) : 0.0f;
-    l = l * f + warp_pairwise_f32(w);
-    m = mn;
-    for (int d = 0; d < D / 32; ++d) o[d] *= f;
-    for (int t = 0; t < 32; ++t) {
-      const float wt = __shfl_sync(0xffffffffu, w, t);
-      if (wt == 0.0f) continue;
-      const uint8_t* vc = p.c.v_codes + (row0 + j0 + t) * D;
-      const float wv = wt * kv_pow2(vx[(j0 + t) / 64]);
-      for (int d = 0; d < D / 32; ++d) o[d] += wv * e4m3_to_f32(vc[d * 32 + lane]);
-    }
-  }
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + b * p.os[0] + i * p.os[1] + hq * p.os[2];
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  for (int d = 0; d < D / 32; ++d) out[d * 32 + lane] = __float2bfloat16_rn(o[d] * inv);
-  if (p.lse && lane == 0) p.lse[(b * p.heads_q + hq) * p.n_q + i] = l > 0.0f ? m + logf(l) : -INFINITY;
-}
-
-cudaError_t launch_kv8_attention(const Kv8Attn& p, cudaStream_t s, const char** why) {
-  if (p.n_q * (p.heads_q / p.c.heads) > 16) return launch_kv8_tiles(p, 1, nullptr, s, why);
-  *why = "k_kv8_attn launch";
-  const dim3 grid((unsigned)ceil_div(p.n_q, 4), (unsigned)p.heads_q, (unsigned)p.c.batch);
-  if (p.c.dim == 64)
-    k_kv8_attn<64><<<grid, 128, 0, s>>>(p);
-  else
-    k_kv8_attn<128><<<grid, 128, 0, s>>>(p);
-  return cudaGetLastError();
-}
-
-size_t kv8_workspace_bytes(int64_t batch, int64_t heads_q, int64_t n_q, int dim) {
-  (void)batch, (void)heads_q, (void)n_q, (void)dim;
-  return 256;
 }
 
 }  // namespace sb

@@ -30,6 +30,17 @@ __device__ __forceinline__ float pow2_byte(int byte) {  // 2^(byte - 127)
   return byte <= 0 ? 0x1p-127f : __uint_as_float((uint32_t)byte << 23);
 }
 
+constexpr float kRise = 8.0f;  // log2 of how far a weight may pass 1 before the running maximum moves
+constexpr int kFewRows = 16;   // rows of a key head up to which the streaming kernel serves
+
+// The power of two that brings a row of queries with largest magnitude `a` (bf16 bits) to [2^14, 2^15),
+// and the factor of the scores that takes it and log2(e) back. An Inf or NaN stays one.
+__device__ __forceinline__ float query_scale(float scale, uint32_t a, float& factor) {
+  const int e = min(141 - (int)(a >> 7), 127);  // 14 - floor(log2 a)
+  factor = __uint_as_float((uint32_t)(e + 127) << 23);
+  return scale * 1.4426950408889634f * __uint_as_float((uint32_t)max(127 - e, 1) << 23);
+}
+
 // One sequence: tokens held, queries, and the position of a query token.
 struct Span {
   int len, nq, causal;
@@ -83,8 +94,7 @@ __host__ __device__ inline int64_t part_rows(const Kv8Attn& p) {
 __device__ __forceinline__ int64_t part_index(const Kv8Attn& p, int split, int64_t b, int64_t hk, int64_t r) {
   return (split * p.c.batch * p.c.heads + b * p.c.heads + hk) * (p.n_q * (p.heads_q / p.c.heads)) + r;
 }
-__device__ __forceinline__ float* part_row(const Kv8Attn& p, float* part, int splits, int split, int64_t b, int64_t hk,
-                                           int64_t r) {
+__device__ __forceinline__ float* part_row(const Kv8Attn& p, float* part, int split, int64_t b, int64_t hk, int64_t r) {
   return part + part_index(p, split, b, hk, r) * p.c.dim;
 }
 __device__ __forceinline__ float* part_lse(const Kv8Attn& p, float* part, int splits, int split, int64_t b, int64_t hk,

@@ -33,7 +33,6 @@ constexpr uint32_t kRegsSoft = 192, kRegsConv = 88, kRegsMma = 40;
 constexpr int kRegsNeeded = (int)(kRegsSoft * 256 + kRegsConv * 128 + kRegsMma * 128);
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kSlab = 16384;  // 128 rows x 64 fp16, 128B swizzle
-constexpr float kRise = 8.0f;
 
 struct TileExp {  // a key tile's two blocks: 2^ek, ev and 2^-ev (relative)
   float k[2], v[2], iv[2];
@@ -184,9 +183,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
                                    __vmaxu2(u[c].z & 0x7fff7fffu, u[c].w & 0x7fff7fffu)));
         }
         a = max(a & 0xffffu, a >> 16);
-        const int e = min(141 - (int)(a >> 7), 127);  // 14 - floor(log2 max), the factor's exponent
-        const float f = __uint_as_float((uint32_t)(e + 127) << 23);
-        qc = p.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 - e > 0 ? 127 - e : 1) << 23);
+        float f;
+        qc = query_scale(p.scale, a, f);
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
           float v[8];
@@ -273,9 +271,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
         *abort = 1;
       } else {
         tc_fence_after();
-        // l > 0, or nothing is visible (or the row is NaN, and stays it)
-        const float inv = l > 0.0f ? __uint_as_float((uint32_t)max(sh.evmax, 1) << 23) / l : 0.0f;
-        const float lse2 = l > 0.0f ? m + log2f(l) : -INFINITY;
+        // nothing visible: zeros and -inf; a NaN row has a NaN sum and stays NaN
+        const float inv = l > 0.0f ? __uint_as_float((uint32_t)max(sh.evmax, 1) << 23) / l : l;
+        const float lse2 = l > 0.0f ? m + log2f(l) : l == 0.0f ? -INFINITY : l;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -297,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
               dst[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
                                   pack_bf16x2(o[8 * i + 4], o[8 * i + 5]), pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
           } else {
-            float* dst = part_row(p, part, splits, split, b, hk, r) + 32 * c;
+            float* dst = part_row(p, part, split, b, hk, r) + 32 * c;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               reinterpret_cast<uint4*>(dst)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);

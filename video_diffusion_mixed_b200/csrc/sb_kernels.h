@@ -228,7 +228,8 @@ struct Kv8Attn {
   WsHeader* hdr;
 };
 cudaError_t launch_kv8_store(const Kv8Store& p, cudaStream_t s);
-cudaError_t launch_kv8_attention(const Kv8Attn& p, cudaStream_t s, const char** why);
+constexpr size_t kKv8PartOffset = 256;  // partial results in the attention workspace, behind the header
+cudaError_t launch_kv8_attention(const Kv8Attn& p, void* part, cudaStream_t s, const char** why);
 cudaError_t launch_kv8_tiles(const Kv8Attn& p, int splits, float* part, cudaStream_t s, const char** why);
 size_t kv8_workspace_bytes(int64_t batch, int64_t heads_q, int64_t n_q, int dim);
 
