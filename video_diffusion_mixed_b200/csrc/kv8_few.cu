@@ -2,21 +2,25 @@
 // the tokens being generated), and the join of partial results.
 //
 // Bound by reading the visible part of the cache once (2 D bytes a token and head), so the keys are
-// split over many blocks and each warp streams 32-token steps of its block's share on its own: a thread
-// copies (cp.async) and reads back its own pieces, three steps deep, with no barrier before the end.
-// The products run on 16-row matrix instructions in fp16 (codes are exact there) with FP32 sums:
+// split over many blocks, and each warp streams 32-token steps of its block's share on its own: one TMA
+// box of keys and one of values a step, three steps deep, no barrier between warps before the end.
+// The products run on 16 x 8 matrix instructions in fp16 (codes are exact there) with FP32 sums, with the
+// cache on the side of 16 and the query rows on the side of 8, so that few rows waste little:
 //
-//   S [16 rows x 8 tokens] += Q K^T: a thread's fragment holds one token's channels 16t + 4i .. + 3 of a
+//   S^T [16 tokens x 8 rows] += K Q^T: a thread's fragment holds a token's channels 16t + 4i .. + 3 of a
 //      64-channel chunk (the order of a contraction is free), 16 contiguous bytes of the cache;
-//   O [16 rows x 8 channels] += w V: the weights are already the left operand's fragment; on the right a
-//      thread takes D / 8 contiguous channels of four tokens, so column g of tile i is channel
-//      g D / 8 + i, and the bytes of two neighbouring tokens are interleaved to fp16 pairs.
+//   O^T [16 channels x 8 rows] += V^T w^T: a thread takes D / 8 contiguous channels of four tokens; the bytes
+//      of two neighbouring tokens are interleaved to fp16 pairs, and the weights change from S^T's
+//      fragment to a right operand by 8 x 8 transposes in the register file.
 //
 // Block scales, the running maximum and its rare moves are those of the tensor-core kernel beside it.
+#include <cudaTypedefs.h>
+
 #include "kv8.cuh"
 #include "launch_util.h"
 #include "sb_device.cuh"
 #include "sb_kernels.h"
+#include "tmap.h"
 
 namespace sb {
 namespace kv8 {
@@ -25,6 +29,8 @@ constexpr int kFewWarps = 4;
 constexpr int kFewThreads = kFewWarps * 32;
 constexpr int kFewSlots = 3;
 constexpr int kStep = 32;  // tokens
+constexpr uint64_t kFewWaitNs = 2000000000ull;  // far above any legitimate wait
+constexpr uint64_t kFewDrainNs = 20000000ull;
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
@@ -38,25 +44,35 @@ __device__ __forceinline__ float fast_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-template <int BYTES>
-__device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(live ? BYTES : 0)
-               : "memory");
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {  // 8 x 8 matrix of 16-bit values
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+
+struct FewMaps {
+  CUtensorMap k, v;  // {dim, capacity, batch * heads}, box of kStep tokens
+};
+
+// Byte `c` of token row `r` in a box: rows of 128 bytes under the 128B swizzle, of 64 under the 64B one.
+template <int D>
+__device__ __forceinline__ uint32_t box_addr(uint32_t box, int r, int c) {
+  const int x = D == 128 ? r & 7 : (r >> 1) & 3;
+  return box + (uint32_t)(r * D + (((c >> 4) ^ x) << 4) + (c & 15));
 }
 
 template <int D>
-struct FewSlot {  // one step of every warp; [thread] is that thread's own
-  uint4 k[4][D / 64][kFewThreads];                    // token 8j + g, channels 64c + 16t .. + 15
-  uint8_t v[2][4][kFewThreads][D / 8];                // tokens 16s + {2t, 2t+1, 2t+8, 2t+9}, channels g D/8 ..
-};
+constexpr int few_smem() {
+  return kFewWarps * kFewSlots * 2 * kStep * D + 1024 + kFewWarps * kFewSlots * 8;
+}
 
-// WIDE: 9 to 16 rows; otherwise the lower half of the matrix instruction's rows stays empty.
-template <int D, bool WIDE>
-__global__ void __launch_bounds__(kFewThreads) k_kv8_few(const Kv8Attn p, int splits, float* part) {
-  extern __shared__ __align__(16) uint8_t few_smem[];
-  FewSlot<D>* ring = reinterpret_cast<FewSlot<D>*>(few_smem);
-  constexpr int kR = WIDE ? 2 : 1;  // rows g (and g + 8) of this thread
-  constexpr int kC = D / 64, kN = D / 8;
+// NT tiles of eight query rows.
+template <int D, int NT>
+__global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__ FewMaps tm, const Kv8Attn p, int splits,
+                                                         float* part) {
+  extern __shared__ uint8_t few_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(few_smem_raw) + 1023) & ~(uintptr_t)1023);
+  constexpr int kC = D / 64, kN = D / 8, kBox = kStep * D;
   if (p.prec && *p.prec == SB_SKIP) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int group = (int)(p.heads_q / p.c.heads);
@@ -70,48 +86,39 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const Kv8Attn p, int sp
   const KeyTiles kt = key_tiles(p, pmin, pmax, 64);
   const int i0 = (int)((int64_t)kt.n * split / splits), i1 = (int)((int64_t)kt.n * (split + 1) / splits);
   const int steps = 2 * (i1 - i0);
-  const int64_t head0 = (b * p.c.heads + hk) * p.c.capacity;
-  const uint8_t* kc = p.c.k_codes + head0 * D;
-  const uint8_t* vc = p.c.v_codes + head0 * D;
-  const uint8_t* kx = p.c.k_exp + head0 / 64;
-  const uint8_t* vx = p.c.v_exp + head0 / 64;
+  const int head = (int)(b * p.c.heads + hk);
+  const uint8_t* kx = p.c.k_exp + (int64_t)head * (p.c.capacity / 64);
+  const uint8_t* vx = p.c.v_exp + (int64_t)head * (p.c.capacity / 64);
 
-  auto fetch = [&](int slot, int q) {
-    if (q < steps) {
-      FewSlot<D>& o = ring[slot];
-      const int j0 = kt.tile(i0 + (q >> 1)) * 64 + (q & 1) * kStep;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int tok = j0 + 8 * j + g;
-#pragma unroll
-        for (int c = 0; c < kC; ++c)
-          cp_async_or_zero<16>(smem_u32(&o.k[j][c][tid]), kc + (int64_t)tok * D + 64 * c + 16 * t, tok < sp.len);
-      }
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int tok = j0 + 16 * s + 2 * t + (i & 1) + 8 * (i >> 1);
-          cp_async_or_zero<kN>(smem_u32(&o.v[s][i][tid][0]), vc + (int64_t)tok * D + kN * g, tok < sp.len);
-        }
-      }
-    }
-    cp_async_commit();
+  // this warp's ring: slot s holds a box of keys, then one of values
+  const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kFewSlots * 2 * kBox);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kFewWarps * kFewSlots * 2 * kBox) + warp * kFewSlots;
+  auto fetch = [&](int slot, int q) {  // one lane
+    if (q >= steps) return;
+    const int j0 = kt.tile(i0 + (q >> 1)) * 64 + (q & 1) * kStep;
+    const uint32_t box = ring + (uint32_t)(slot * 2 * kBox), bar = smem_u32(&full[slot]);
+    mbar_arrive_expect_tx(&full[slot], 2 * kBox);
+    tma_load_3d(box, &tm.k, bar, 0, j0, head);
+    tma_load_3d(box + kBox, &tm.v, bar, 0, j0, head);
   };
-#pragma unroll
-  for (int u = 0; u < kFewSlots; ++u) fetch(u, warp + u * kFewWarps);
+  if (lane == 0) {
+    for (int u = 0; u < kFewSlots; ++u) mbar_init(&full[u], 1);
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    for (int u = 0; u < kFewSlots; ++u) fetch(u, warp + u * kFewWarps);
+  }
+  __syncwarp();
 
-  // queries: rows g and g + 8 as the left operand
-  uint32_t qf[kC][4][2][kR];
-  float qc[kR];
-  int pos[kR];
+  // queries as the right operand: row 8n + g, channels 64c + 16t + 4i .. + 3
+  uint32_t qf[NT][kC][4][2];
+  float qc[NT][2];  // rows 8n + 2t, 8n + 2t + 1
+  int pos[NT][2];
 #pragma unroll
-  for (int h = 0; h < kR; ++h) {
-    const int r = g + 8 * h;
+  for (int n = 0; n < NT; ++n) {
+    const int r = g + 8 * n;
     const bool live = r < rows;
     const int tok = live ? r / group : 0;
     const int64_t hq = hk * group + (live ? r - tok * group : 0);
-    pos[h] = live ? sp.pos(tok) : -1;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + b * p.qs[0] + tok * p.qs[1] + hq * p.qs[2];
     uint4 u[kC][2];
     uint32_t a = 0;
@@ -128,144 +135,200 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const Kv8Attn p, int sp
     a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
     a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
     float f;
-    qc[h] = query_scale(p.scale, a, f);
+    const float back = query_scale(p.scale, a, f);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int rr = 8 * n + 2 * t + e;
+      qc[n][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + e));
+      pos[n][e] = rr < rows ? sp.pos(rr / group) : -1;
+    }
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float v[8];
         unpack8(u[c][i], v);
-        qf[c][2 * i][0][h] = pack_f16(v[0] * f, v[1] * f);
-        qf[c][2 * i][1][h] = pack_f16(v[2] * f, v[3] * f);
-        qf[c][2 * i + 1][0][h] = pack_f16(v[4] * f, v[5] * f);
-        qf[c][2 * i + 1][1][h] = pack_f16(v[6] * f, v[7] * f);
+        qf[n][c][2 * i][0] = pack_f16(v[0] * f, v[1] * f);
+        qf[n][c][2 * i][1] = pack_f16(v[2] * f, v[3] * f);
+        qf[n][c][2 * i + 1][0] = pack_f16(v[4] * f, v[5] * f);
+        qf[n][c][2 * i + 1][1] = pack_f16(v[6] * f, v[7] * f);
       }
     }
   }
-  // the largest exponent of V over the block's share (after the first copies are on their way)
+  // the largest exponent of V over the block's share (while the first boxes are on their way)
   const int blocks = (sp.len + 63) >> 6;
   int evmax = 0;
   for (int i = lane; i < i1 - i0; i += 32) {
     const int blk = kt.tile(i0 + i);
-    if (blk < blocks) evmax = max(evmax, (int)vx[blk]);
+    if (blk < blocks) evmax = max(evmax, (int)__ldg(vx + blk));
   }
 #pragma unroll
   for (int s = 16; s >= 1; s >>= 1) evmax = max(evmax, __shfl_xor_sync(0xffffffffu, evmax, s));
 
-  float m[kR], l[kR], o[kN][2 * kR];
+  float m[NT][2], l[NT][2], o[kN / 2][NT][4];
 #pragma unroll
-  for (int h = 0; h < kR; ++h) m[h] = -INFINITY, l[h] = 0.0f;
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-  for (int i = 0; i < kN; ++i)
+    for (int e = 0; e < 2; ++e) m[n][e] = -INFINITY, l[n][e] = 0.0f;
 #pragma unroll
-    for (int h = 0; h < 2 * kR; ++h) o[i][h] = 0.0f;
+  for (int i = 0; i < kN / 2; ++i)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][n][e] = 0.0f;
 
   int slot = 0;
+  uint32_t ph = 0;
+  bool late = false;
   for (int q = warp; q < steps; q += kFewWarps) {
     const int blk = kt.tile(i0 + (q >> 1)), j0 = blk * 64 + (q & 1) * kStep;
-    const int ke = blk < blocks ? (int)__ldg(kx + blk) : 127, ve = blk < blocks ? (int)__ldg(vx + blk) : 0;
-    asm volatile("cp.async.wait_group %0;" ::"n"(kFewSlots - 1) : "memory");
-    const FewSlot<D>& d = ring[slot];
-    float x[4][4];
+    const int ke = (int)__ldg(kx + blk), ve = (int)__ldg(vx + blk);  // a tile starts below len
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[slot], ph, nullptr, kFewWaitNs))) {
+      if (lane == 0) set_error(p.hdr, SB_ETIMEOUT);
+      late = true;
+      break;
+    }
+    const uint32_t kbox = ring + (uint32_t)(slot * 2 * kBox), vbox = kbox + kBox;
+    float x[2][NT][4];  // tokens 16a + g (rows 2t, 2t + 1), 16a + g + 8
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float acc[4] = {};
+    for (int a = 0; a < 2; ++a) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[a][n][e] = 0.0f;
 #pragma unroll
       for (int c = 0; c < kC; ++c) {
-        const uint4 w = d.k[j][c][tid];
+        const uint4 lo = ld_shared_v4(box_addr<D>(kbox, 16 * a + g, 64 * c + 16 * t));
+        const uint4 hi = ld_shared_v4(box_addr<D>(kbox, 16 * a + g + 8, 64 * c + 16 * t));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t k = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
-          mma_16816(acc, qf[c][i][0][0], WIDE ? qf[c][i][0][kR - 1] : 0u, qf[c][i][1][0],
-                    WIDE ? qf[c][i][1][kR - 1] : 0u, e4m3x2_f16x2(k), e4m3x2_f16x2(k >> 16));
+          const uint32_t k0 = i == 0 ? lo.x : i == 1 ? lo.y : i == 2 ? lo.z : lo.w;
+          const uint32_t k1 = i == 0 ? hi.x : i == 1 ? hi.y : i == 2 ? hi.z : hi.w;
+          const uint32_t a0 = e4m3x2_f16x2(k0), a1 = e4m3x2_f16x2(k1);
+          const uint32_t a2 = e4m3x2_f16x2(k0 >> 16), a3 = e4m3x2_f16x2(k1 >> 16);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_16816(x[a][n], a0, a1, a2, a3, qf[n][c][i][0], qf[n][c][i][1]);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[j][i] = acc[i];
     }
     const int rel = max(ve - evmax, -64);
-    const float ev = (float)rel, iv = __uint_as_float((uint32_t)(127 - rel) << 23);
+    const float ev = (float)rel, iv = __uint_as_float((uint32_t)(127 - rel) << 23), ks = pow2_byte(ke);
     const bool mask = tile_needs_mask(p, j0, kStep, pmin, pmax);
-    uint32_t w[4][kR];
+    uint32_t w[2][NT][2];
 #pragma unroll
-    for (int h = 0; h < kR; ++h) {
-      if (mask) {
+    for (int n = 0; n < NT; ++n) {
+      float f[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+      for (int e = 0; e < 2; ++e) {
+        if (mask) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (!key_visible(p, pos[h], j0 + 8 * j + 2 * t + i)) x[j][2 * h + i] = -INFINITY;
+          for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (!key_visible(p, pos[n][e], j0 + 16 * a + 8 * h + g)) x[a][n][2 * h + e] = -INFINITY;
+        }
+        float mx = fmaxf(fmaxf(x[0][n][e], x[0][n][2 + e]), fmaxf(x[1][n][e], x[1][n][2 + e]));
+#pragma unroll
+        for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+        const float c = fminf(fmaxf(qc[n][e] * ks, 0x1p-126f), 0x1p126f);
+        const float mn = fmaxf(m[n][e], fmaf(mx, c, ev));
+        f[e] = 1.0f;
+        if (mn > m[n][e] + kRise) {
+          f[e] = fast_ex2(m[n][e] - mn);
+          m[n][e] = mn;
+          l[n][e] *= f[e];
+        }
+        const float add = ev - (m[n][e] == -INFINITY ? 0.0f : m[n][e]);
+        float sum = 0.0f;
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            x[a][n][2 * h + e] = fast_ex2(fmaf(x[a][n][2 * h + e], c, add));
+            sum += x[a][n][2 * h + e];
+          }
+        }
+        l[n][e] = fmaf(sum, iv, l[n][e]);  // this lane's tokens
       }
-      float mx = -INFINITY;
+      if (__any_sync(0xffffffffu, f[0] != 1.0f || f[1] != 1.0f)) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) mx = max3(mx, x[j][2 * h], x[j][2 * h + 1]);
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float c = fminf(fmaxf(qc[h] * pow2_byte(ke), 0x1p-126f), 0x1p126f);
-      const float mn = fmaxf(m[h], fmaf(mx, c, ev));
-      if (__any_sync(0xffffffffu, mn > m[h] + kRise)) {
-        const float f = mn == m[h] ? 1.0f : fast_ex2(m[h] - mn);
-        m[h] = mn;
-        l[h] *= f;
-#pragma unroll
-        for (int i = 0; i < kN; ++i) o[i][2 * h] *= f, o[i][2 * h + 1] *= f;
+        for (int i = 0; i < kN / 2; ++i) {
+          o[i][n][0] *= f[0], o[i][n][1] *= f[1];
+          o[i][n][2] *= f[0], o[i][n][3] *= f[1];
+        }
       }
-      const float add = ev - (m[h] == -INFINITY ? 0.0f : m[h]);
-      float sum = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float a = fast_ex2(fmaf(x[j][2 * h], c, add)), e = fast_ex2(fmaf(x[j][2 * h + 1], c, add));
-        sum += a + e;
-        w[j][h] = pack_f16(a, e);
-      }
-      l[h] = fmaf(sum, iv, l[h]);
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) w[a][n][h] = transpose8(pack_f16(x[a][n][2 * h], x[a][n][2 * h + 1]));
     }
-    const bool far = ve < evmax - 64;  // more than 2^64 below the largest block: counts as zero
+    // zero what must not meet a weight of zero: codes past the end (they may be NaN), and blocks more
+    // than 2^64 below the largest
+    const int fine = ve < evmax - 64 ? 0 : sp.len - j0;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int a = 0; a < 2; ++a) {
+      uint32_t e[4][kN / 4];  // tokens 16a + {2t, 2t+1, 2t+8, 2t+9}, channels kN g ..
 #pragma unroll
-      for (int c = 0; c < kN / 4; ++c) {  // four channels of four tokens
-        uint32_t e[4];
+      for (int i = 0; i < 4; ++i) {
+        const int tok = 16 * a + 2 * t + (i & 1) + 8 * (i >> 1);
+        const uint32_t addr = box_addr<D>(vbox, tok, kN * g);
+        if constexpr (D == 128) {
+          const uint4 v = ld_shared_v4(addr);
+          e[i][0] = v.x, e[i][1] = v.y, e[i][2] = v.z, e[i][3] = v.w;
+        } else {
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(e[i][0]), "=r"(e[i][1]) : "r"(addr));
+        }
+        if (fine < kStep && tok >= fine) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = far ? 0u : *reinterpret_cast<const uint32_t*>(&d.v[s][i][tid][4 * c]);
-        const uint32_t p0 = __byte_perm(e[0], e[1], 0x5140), p1 = __byte_perm(e[0], e[1], 0x7362);
-        const uint32_t r0 = __byte_perm(e[2], e[3], 0x5140), r1 = __byte_perm(e[2], e[3], 0x7362);
+          for (int c = 0; c < kN / 4; ++c) e[i][c] = 0u;
+        }
+      }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t lo = i < 2 ? p0 : p1, hi = i < 2 ? r0 : r1;
-          float acc[4];
+      for (int c = 0; c < kN / 4; ++c) {
 #pragma unroll
-          for (int h = 0; h < 4; ++h) acc[h] = h < 2 * kR ? o[4 * c + i][h < 2 * kR ? h : 0] : 0.0f;
-          mma_16816(acc, w[2 * s][0], WIDE ? w[2 * s][kR - 1] : 0u, w[2 * s + 1][0], WIDE ? w[2 * s + 1][kR - 1] : 0u,
-                    e4m3x2_f16x2(i & 1 ? lo >> 16 : lo), e4m3x2_f16x2(i & 1 ? hi >> 16 : hi));
+        for (int h = 0; h < 2; ++h) {  // channels 4c + 2h (row g) and 4c + 2h + 1 (row g + 8)
+          const uint32_t lo = __byte_perm(e[0][c], e[1][c], h ? 0x7362 : 0x5140);
+          const uint32_t hi = __byte_perm(e[2][c], e[3][c], h ? 0x7362 : 0x5140);
+          const uint32_t a0 = e4m3x2_f16x2(lo), a1 = e4m3x2_f16x2(lo >> 16);
+          const uint32_t a2 = e4m3x2_f16x2(hi), a3 = e4m3x2_f16x2(hi >> 16);
 #pragma unroll
-          for (int h = 0; h < 2 * kR; ++h) o[4 * c + i][h] = acc[h];
+          for (int n = 0; n < NT; ++n) mma_16816(o[2 * c + h][n], a0, a1, a2, a3, w[a][n][0], w[a][n][1]);
         }
       }
     }
-    fetch(slot, q + kFewSlots * kFewWarps);  // this thread has read its pieces of the slot
-    slot = slot + 1 == kFewSlots ? 0 : slot + 1;
+    __syncwarp();  // every lane has read the slot
+    if (lane == 0) fetch(slot, q + kFewSlots * kFewWarps);
+    if (++slot == kFewSlots) slot = 0, ph ^= 1u;
   }
-  cp_async_wait_all();
+  if (late) {  // what is still in flight lands before the memory is used again
+    for (int u = 0; u < kFewSlots; ++u, ph ^= slot == kFewSlots - 1, slot = slot + 1 == kFewSlots ? 0 : slot + 1)
+      mbar_wait_bounded(&full[slot], ph, nullptr, kFewDrainNs);
+  }
+  asm volatile("griddepcontrol.launch_dependents;");  // the join waits for this launch's end itself
 
   // join the warps: sums over the lanes of a row, then warp after warp in shared memory
 #pragma unroll
-  for (int h = 0; h < kR; ++h) {
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-  }
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int s = 4; s < 32; s <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], s);
   __syncthreads();  // the ring's memory is reused
-  float* sm = reinterpret_cast<float*>(few_smem);  // [warp][row] m, then l, then [warp][row][D] outputs
-  float* sl = sm + kFewWarps * 16;
-  float* so = sl + kFewWarps * 16;
+  constexpr int kRows = 8 * NT;
+  float* sm = reinterpret_cast<float*>(smem);  // [warp][row] m, then l, then [warp][row][D + 4] outputs
+  float* sl = sm + kFewWarps * kRows;
+  float* so = sl + kFewWarps * kRows;
 #pragma unroll
-  for (int h = 0; h < kR; ++h) {
-    const int r = g + 8 * h;
-    if (t == 0) sm[warp * 16 + r] = m[h], sl[warp * 16 + r] = l[h];
+  for (int n = 0; n < NT; ++n) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i)  // accumulator columns 2t, 2t + 1 of tile i: channels kN * column + i
+    for (int e = 0; e < 2; ++e) {
+      const int r = 8 * n + 2 * t + e;
+      if (g == 0) sm[warp * kRows + r] = m[n][e], sl[warp * kRows + r] = l[n][e];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) so[(warp * 16 + r) * (D + 4) + kN * (2 * t + e) + i] = o[i][2 * h + e];
+      for (int i = 0; i < kN / 2; ++i)
+        *reinterpret_cast<float2*>(&so[(warp * kRows + r) * (D + 4) + kN * g + 2 * i]) =
+            make_float2(o[i][n][e], o[i][n][2 + e]);
+    }
   }
   __syncthreads();
   const float unit = __uint_as_float((uint32_t)max(evmax, 1) << 23);
@@ -273,15 +336,14 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const Kv8Attn p, int sp
     const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
     float mx = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kFewWarps; ++w) mx = fmaxf(mx, sm[w * 16 + r]);
+    for (int w = 0; w < kFewWarps; ++w) mx = fmaxf(mx, sm[w * kRows + r]);
     float tot = 0.0f, y[4] = {};
 #pragma unroll
     for (int w = 0; w < kFewWarps; ++w) {
-      const float mw = sm[w * 16 + r], f = mw == -INFINITY ? 0.0f : fast_ex2(mw - mx);
-      const float* src = so + (w * 16 + r) * (D + 4) + c;
-      tot = fmaf(sl[w * 16 + r], f, tot);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = fmaf(src[e], f, y[e]);
+      const float mw = sm[w * kRows + r], f = mw == -INFINITY ? 0.0f : fast_ex2(mw - mx);
+      const float4 v = *reinterpret_cast<const float4*>(so + (w * kRows + r) * (D + 4) + c);
+      tot = fmaf(sl[w * kRows + r], f, tot);
+      y[0] = fmaf(v.x, f, y[0]), y[1] = fmaf(v.y, f, y[1]), y[2] = fmaf(v.z, f, y[2]), y[3] = fmaf(v.w, f, y[3]);
     }
     // nothing visible: zeros and -inf; a NaN row has a NaN sum and stays NaN
     const float inv = tot > 0.0f ? unit / tot : tot;
@@ -302,76 +364,96 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const Kv8Attn p, int sp
   }
 }
 
-// Joins the parts of a row: out = sum 2^(lse_s - max) o_s / sum 2^(lse_s - max). A warp per row, a lane D / 32
-// channels; parts that saw no key have lse -inf.
+// Joins the parts of a row: out = sum 2^(lse_s - max) o_s / sum 2^(lse_s - max). A block per row; its
+// warps take the parts in turn, a lane D / 32 channels, and meet in shared memory in a fixed order. Parts
+// that saw no key have lse -inf.
+constexpr int kJoinWarps = 8;
+
 template <int D>
-__global__ void __launch_bounds__(128) k_kv8_join(const Kv8Attn p, int splits, float* part) {
+__global__ void __launch_bounds__(kJoinWarps * 32) k_kv8_join(const Kv8Attn p, int splits, float* part) {
+  __shared__ float sy[kJoinWarps][D], st[kJoinWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (p.prec && *p.prec == SB_SKIP) return;
-  const int lane = threadIdx.x & 31;
+  constexpr int kE = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = (int)(p.heads_q / p.c.heads);
   const int64_t per = p.n_q * group;  // rows of a sequence and key head
-  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (i >= part_rows(p)) return;
+  const int64_t i = blockIdx.x;
   const int64_t bh = i / per, r = i - bh * per, b = bh / p.c.heads, hk = bh - b * p.c.heads;
   const int64_t tok = r / group, hq = hk * group + r - tok * group;
   if (tok >= sequence_span(p, b).nq) return;
   float mx = -INFINITY;
-  bool nan = false;
-  for (int s = lane; s < splits; s += 32) {
-    const float v = __ldcg(part_lse(p, part, splits, s, b, hk, r));
-    nan = nan || v != v;
-    mx = fmaxf(mx, v);
-  }
-  mx = warp_max_f32(mx);
-  nan = __any_sync(0xffffffffu, nan);
-  float tot = 0.0f, y[D / 32] = {};
-  if (mx != -INFINITY || nan) {
+  for (int s = lane; s < splits; s += 32) mx = fmaxf(mx, __ldcg(part_lse(p, part, splits, s, b, hk, r)));
+  mx = warp_max_f32(mx);  // NaN parts are ignored here and make the sums NaN below
+  const float base = mx == -INFINITY ? 0.0f : mx;
+  float tot = 0.0f, y[kE] = {};
 #pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-      const float f = fast_ex2(__ldcg(part_lse(p, part, splits, s, b, hk, r)) - mx);
-      const float* src = part_row(p, part, s, b, hk, r) + lane * (D / 32);
-      tot += f;
-      if constexpr (D == 128) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-        y[0] = fmaf(v.x, f, y[0]), y[1] = fmaf(v.y, f, y[1]), y[2] = fmaf(v.z, f, y[2]), y[3] = fmaf(v.w, f, y[3]);
-      } else {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-        y[0] = fmaf(v.x, f, y[0]), y[1] = fmaf(v.y, f, y[1]);
-      }
+  for (int s = warp; s < splits; s += kJoinWarps) {
+    const float f = fast_ex2(__ldcg(part_lse(p, part, splits, s, b, hk, r)) - base);
+    const float* src = part_row(p, part, s, b, hk, r) + lane * kE;
+    tot += f;
+    if constexpr (D == 128) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+      y[0] = fmaf(v.x, f, y[0]), y[1] = fmaf(v.y, f, y[1]), y[2] = fmaf(v.z, f, y[2]), y[3] = fmaf(v.w, f, y[3]);
+    } else {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+      y[0] = fmaf(v.x, f, y[0]), y[1] = fmaf(v.y, f, y[1]);
     }
   }
-  const float inv = tot > 0.0f ? 1.0f / tot : tot;
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + b * p.os[0] + tok * p.os[1] + hq * p.os[2] + lane * (D / 32);
 #pragma unroll
-  for (int c = 0; c < D / 64; ++c)
-    reinterpret_cast<uint32_t*>(dst)[c] =
-        pack_bf16x2(__float_as_uint(y[2 * c] * inv), __float_as_uint(y[2 * c + 1] * inv));
-  if (p.lse && lane == 0)
+  for (int e = 0; e < kE; ++e) sy[warp][lane * kE + e] = y[e];
+  if (lane == 0) st[warp] = tot;
+  __syncthreads();
+  const int c = threadIdx.x * 2;  // two channels a thread
+  if (c >= D) return;
+  float t = 0.0f, a0 = 0.0f, a1 = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) t += st[w], a0 += sy[w][c], a1 += sy[w][c + 1];
+  const float inv = t > 0.0f ? 1.0f / t : t;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + b * p.os[0] + tok * p.os[1] + hq * p.os[2] + c;
+  *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(__float_as_uint(a0 * inv), __float_as_uint(a1 * inv));
+  if (p.lse && c == 0)
     p.lse[(b * p.heads_q + hq) * p.n_q + tok] =
-        tot > 0.0f ? (mx + log2f(tot)) * 0.6931471805599453f : nan ? NAN : -INFINITY;
+        t > 0.0f ? (mx + log2f(t)) * 0.6931471805599453f : t == 0.0f ? -INFINITY : t;
 }
 
-template <int D, bool WIDE>
+static bool cache_map(CUtensorMap* m, const uint8_t* base, const sb_kv8& c) {
+  auto fn = tmap_encoder();
+  cuuint64_t dims[3] = {(cuuint64_t)c.dim, (cuuint64_t)c.capacity, (cuuint64_t)(c.batch * c.heads)};
+  cuuint64_t strides[2] = {(cuuint64_t)c.dim, (cuuint64_t)(c.dim * c.capacity)};
+  cuuint32_t box[3] = {(cuuint32_t)c.dim, kStep, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, c.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NT>
 static cudaError_t launch_few(const Kv8Attn& p, int splits, float* part, cudaStream_t s) {
-  constexpr int kBytes = (int)(kFewSlots * sizeof(FewSlot<D>));
-  static_assert(kBytes >= (int)sizeof(float) * (kFewWarps * 16 * 2 + kFewWarps * 16 * (D + 4)), "join in the ring");
+  constexpr int kBytes = few_smem<D>() + 1024;  // + alignment of the dynamic base
+  static_assert(kFewSlots * kFewWarps * 2 * kStep * D >= 4 * (kFewWarps * 16 * NT + kFewWarps * 8 * NT * (D + 4)),
+                "the join fits the ring");
   static std::atomic<uint64_t> attr{0};
-  const cudaError_t e = smem_attr_once(k_kv8_few<D, WIDE>, kBytes, attr);
+  const cudaError_t e = smem_attr_once(k_kv8_few<D, NT>, kBytes, attr);
   if (e != cudaSuccess) return e;
-  k_kv8_few<D, WIDE><<<dim3((unsigned)splits, (unsigned)p.c.heads, (unsigned)p.c.batch), kFewThreads, kBytes, s>>>(
-      p, splits, part);
+  FewMaps tm;
+  if (!cache_map(&tm.k, p.c.k_codes, p.c) || !cache_map(&tm.v, p.c.v_codes, p.c)) return cudaErrorInvalidValue;
+  k_kv8_few<D, NT><<<dim3((unsigned)splits, (unsigned)p.c.heads, (unsigned)p.c.batch), kFewThreads, kBytes, s>>>(
+      tm, p, splits, part);
   return cudaGetLastError();
 }
 
-// How the keys of a call are split. Few rows: enough blocks that their reads fill the memory's queue on
-// every SM, at least 256 tokens each. Many rows: the number of parts with the shortest schedule of 148
-// CTAs, a part costing its key tiles and about three more for its start and its join.
+// How the keys of a call are split. Few rows: one wave of the blocks that fit (two an SM with heads of
+// 128, four with 64), each with at least 256 tokens. Measured with parts for half a wave, one, one and a half,
+// two and four: 32 query and 8 key heads of 128, one sequence of 131071 tokens 62.8 / 52.6 / 62.2 / 56.6 /
+// 65.6 us, eight windows of 4099 tokens 23.5 / 19.4 / 25.1 / 22.1 / 27.5 us; 30 heads of 64, 17776 tokens 23.5 /
+// 21.4 / - / 27.0 us with a half, one and two waves. Many rows: the number of parts with the shortest
+// schedule of 148 CTAs, a part costing its key tiles and about three more for its start and its join.
 static int plan_splits(int64_t batch, int64_t heads, int64_t heads_q, int64_t n_q, int dim, int64_t keys) {
   const int64_t rows = n_q * (heads_q / heads), units = batch * heads;
   const int64_t most = ((int64_t)128 << 20) / (batch * n_q * heads_q * dim * 4);  // 128 MB of partial results
   if (rows <= kFewRows) {
-    const int64_t want = ceil_div(1184, units), fit = keys / 256;
+    const int64_t want = (dim == 64 ? 592 : 296) / units, fit = keys / 256;
     int64_t s = want < fit ? want : fit;
     s = s < most ? s : most;
     return (int)(s > 1 ? s : 1);
@@ -399,15 +481,15 @@ cudaError_t launch_kv8_attention(const Kv8Attn& p, void* part_, cudaStream_t s, 
   cudaError_t e;
   if (rows <= kFewRows) {
     if (p.c.dim == 64)
-      e = rows <= 8 ? launch_few<64, false>(p, splits, part, s) : launch_few<64, true>(p, splits, part, s);
+      e = rows <= 8 ? launch_few<64, 1>(p, splits, part, s) : launch_few<64, 2>(p, splits, part, s);
     else
-      e = rows <= 8 ? launch_few<128, false>(p, splits, part, s) : launch_few<128, true>(p, splits, part, s);
+      e = rows <= 8 ? launch_few<128, 1>(p, splits, part, s) : launch_few<128, 2>(p, splits, part, s);
   } else {
     e = launch_kv8_tiles(p, splits, part, s, why);
   }
   if (e != cudaSuccess || splits == 1) return e;
   *why = "sb_kv8_attention (join)";
-  const LaunchAfter L((unsigned)ceil_div(part_rows(p), 4), 128, 0, s, true);
+  const LaunchAfter L((unsigned)part_rows(p), kJoinWarps * 32, 0, s, true);
   return p.c.dim == 64 ? cudaLaunchKernelEx(&L.cfg, k_kv8_join<64>, p, splits, part)
                        : cudaLaunchKernelEx(&L.cfg, k_kv8_join<128>, p, splits, part);
 }
