@@ -17,8 +17,11 @@
 // largest. The maximum moves only when it would rise by more than 2^8 (fp16 has the room), so the
 // accumulator is rescaled rarely.
 //
-// Warps: 0-3 and 4-7 softmax of the two row tiles, 8-11 codes -> fp16, 12 MMA issue. While one tile's
-// softmax runs, the tensor core works on the other's products. Every wait is bounded (SB_ETIMEOUT).
+// Warps: 0-3 and 4-7 softmax of the two row tiles, 8-11 codes -> fp16, 12 MMA issue. A key tile is taken in
+// two steps of 64 keys (a scale block each). Each row tile has two 64-column score buffers, used in turn,
+// and the weights overwrite their scores: the scores of step u + 2 are computed as soon as the weights of
+// step u have been multiplied, so a softmax finds its next scores ready. Every wait is bounded
+// (SB_ETIMEOUT).
 #include "kv8.cuh"
 #include "launch_util.h"
 #include "sb_device.cuh"
@@ -34,17 +37,21 @@ constexpr int kRegsNeeded = (int)(kRegsSoft * 256 + kRegsConv * 128 + kRegsMma *
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kSlab = 16384;  // 128 rows x 64 fp16, 128B swizzle
 
-struct TileExp {  // a key tile's two blocks: 2^ek, ev and 2^-ev (relative)
-  float k[2], v[2], iv[2];
-  float pad[2];
+struct TileExp {  // a scale block: 2^ek, ev (relative) and 2^-ev
+  float k, v, iv, pad;
 };
 
 struct TileShared {
-  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], drain;
+  uint64_t s_full[2][2];  // row tile, score buffer: the step's scores are complete
+  uint64_t p_full[2][2];  // its weights are written (two buffers: a softmax may be two steps ahead of the MMAs)
+  uint64_t o_done[2];     // and multiplied
+  uint64_t o_full[2];     // those of the last step are
+
   uint32_t tmem;
   int abort;
   int evmax;  // largest exponent byte of V in the CTA's range
-  TileExp exps[4];
+  TileExp exps[4][2];
 };
 
 template <int D>
@@ -94,6 +101,31 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// FP32 pairs, one instruction for two.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2u(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -140,8 +172,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
       mbar_init(&sh.k_empty[s], 1);
       mbar_init(&sh.v_full[s], 128);
       mbar_init(&sh.v_empty[s], 1);
-      mbar_init(&sh.s_full[s], 1);
-      mbar_init(&sh.p_full[s], 128);
+      mbar_init(&sh.s_full[s][0], 1);
+      mbar_init(&sh.s_full[s][1], 1);
+      mbar_init(&sh.p_full[s][0], 128);
+      mbar_init(&sh.p_full[s][1], 128);
+      mbar_init(&sh.o_done[s], 1);
       mbar_init(&sh.o_full[s], 1);
     }
     mbar_init(&sh.drain, 1);
@@ -199,71 +234,80 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
       const uint32_t s_col = tmem + lanes + 128u * t, o_col = tmem + lanes + 256u + (uint32_t)(D * t);
       float m = -INFINITY, l = 0.0f;
       bool ok = true;
-      for (int j = 0; j < n; ++j) {
-        if (!mbar_wait_bounded(&sh.s_full[t], (uint32_t)(j & 1), abort, kWaitNs)) {
+      for (int u = 0; u < 2 * n; ++u) {
+        if (!mbar_wait_bounded(&sh.s_full[t][u & 1], (uint32_t)((u >> 1) & 1), abort, kWaitNs)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        uint32_t x[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32u * c, x[c]);
-        const TileExp& te = sh.exps[j & 3];
-        const float c0 = fminf(fmaxf(qc * te.k[0], 0x1p-126f), 0x1p126f);
-        const float c1 = fminf(fmaxf(qc * te.k[1], 0x1p-126f), 0x1p126f);
+        const uint32_t col = s_col + 64u * (u & 1);
+        uint32_t x[2][32];
+        tmem_ld32(col, x[0]);
+        tmem_ld32(col + 32u, x[1]);
+        const TileExp te = sh.exps[(u >> 1) & 3][u & 1];
+        const float c = fminf(fmaxf(qc * te.k, 0x1p-126f), 0x1p126f);
+        const int j0 = kt.tile(i0 + (u >> 1)) * 128 + (u & 1) * 64;
+        const bool mask = tile_needs_mask(p, j0, 64, pmin, pmax);
         tmem_ld_wait();
-        const int j0 = kt.tile(i0 + j) * 128;
-        if (tile_needs_mask(p, j0, 128, pmin, pmax)) {
+        if (mask) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (!key_visible(p, pos, j0 + 32 * c + i)) x[c][i] = 0xff800000u;
+              if (!key_visible(p, pos, j0 + 32 * h + i)) x[h][i] = 0xff800000u;
         }
-        float mx[2] = {-INFINITY, -INFINITY};
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int i = 0; i < 32; i += 2)
-            mx[c >> 1] = max3(mx[c >> 1], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
-        const float mn = max3(m, fmaf(mx[0], c0, te.v[0]), fmaf(mx[1], c1, te.v[1]));
+            mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]));
+        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+        const float mn = fmaxf(m, fmaf(top, c, te.v));
         if (__any_sync(0xffffffffu, mn > m + kRise)) {
           const float f = mn == m ? 1.0f : ex2(m - mn);
           m = mn;
           l *= f;
-          if (j > 0) {
+          if (u > 0) {
+            ok = mbar_wait_bounded(&sh.o_done[t], (uint32_t)((u - 1) & 1), abort, kWaitNs);
+            if (!__all_sync(0xffffffffu, ok)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
+            for (int h = 0; h < D / 32; ++h) {
               uint32_t o[32];
-              tmem_ld32(o_col + 32u * c, o);
+              tmem_ld32(o_col + 32u * h, o);
               tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st32(o_col + 32u * c, o);
+              tmem_st32(o_col + 32u * h, o);
             }
           }
         }
-        const float base = m == -INFINITY ? 0.0f : m;
-        float sum[2] = {0.0f, 0.0f};
+        const float add = te.v - (m == -INFINITY ? 0.0f : m);
+        const uint64_t cc = pack2(c, c), aa = pack2(add, add);
+        uint64_t sum[2] = {0, 0};
+        uint32_t w[32];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float cc = h ? c1 : c0, dd = te.v[h] - base;
-          uint32_t w[32];
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float a = ex2(fmaf(__uint_as_float(x[2 * h + c][i]), cc, dd));
-              const float d = ex2(fmaf(__uint_as_float(x[2 * h + c][i + 1]), cc, dd));
-              sum[h] += a + d;
-              w[16 * c + i / 2] = pack_f16(a, d);
-            }
-          tmem_st32(s_col + 32u * h, w);
-        }
-        l = fmaf(sum[0], te.iv[0], fmaf(sum[1], te.iv[1], l));
+          for (int i = 0; i < 32; i += 2) {
+            float y0, y1;
+            unpack2(fma2(pack2u(x[h][i], x[h][i + 1]), cc, aa), y0, y1);
+            y0 = ex2(y0);
+            y1 = ex2(y1);
+            sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(y0, y1));
+            w[16 * h + i / 2] = pack_f16(y0, y1);
+          }
+        tmem_st32(col, w);
+        float s0, s1;
+        unpack2(add2(sum[0], sum[1]), s0, s1);
+        l = fmaf(s0 + s1, te.iv, l);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&sh.p_full[t]);
+        mbar_arrive(&sh.p_full[t][u & 1]);
       }
       if (ok && n > 0) ok = mbar_wait_bounded(&sh.o_full[t], 0u, abort, kWaitNs);
       if (!ok) {
@@ -331,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
     }
     const int evmax = sh.evmax;
     uint4 kreg[kPieces], vreg[kPieces];
-    int ke = 127, ve = 0;  // thread h < 2: exponent bytes of the next tile's block h
+    int ke[2] = {127, 127}, ve[2] = {0, 0};  // exponent bytes of the next tile's blocks
     auto fetch = [&](const uint8_t* codes, int j, uint4 (&u)[kPieces]) {
       const int j0 = kt.tile(i0 + j) * 128;
       const uint8_t* src = codes + (head0 + j0) * D;
@@ -342,8 +386,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
       }
     };
     auto fetch_exps = [&](int j) {  // a block past the end: any finite scale
-      const int blk = kt.tile(i0 + j) * 2 + tid;
-      if (tid < 2) ke = blk < blocks ? (int)kx[blk] : 127, ve = blk < blocks ? (int)vx[blk] : 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int blk = kt.tile(i0 + j) * 2 + h;
+        ke[h] = blk < blocks ? (int)kx[blk] : 127;
+        ve[h] = blk < blocks ? (int)vx[blk] : 0;
+      }
     };
     auto put = [&](uint32_t tile, const uint4 (&u)[kPieces]) {
 #pragma unroll
@@ -369,13 +417,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
         ok = false;
         break;
       }
-      if (tid < 2) {  // four tiles' worth: a softmax reads tile j's until its weights are out, and K of
-                      // tile j + 2 comes after that of j + 1 has been multiplied with both row tiles
-        TileExp& te = sh.exps[j & 3];
-        const int rel = max(ve - evmax, -64);
-        te.k[tid] = pow2_byte(ke);
-        te.v[tid] = (float)rel;
-        te.iv[tid] = __uint_as_float((uint32_t)(127 - rel) << 23);
+      const bool far[2] = {ve[0] < evmax - 64, ve[1] < evmax - 64};
+      if (tid < 2) {  // four tiles' worth: a softmax may still read those of tile j - 2 here
+        TileExp& te = sh.exps[j & 3][tid];
+        const int rel = max((tid ? ve[1] : ve[0]) - evmax, -64);
+        te.k = pow2_byte(tid ? ke[1] : ke[0]);
+        te.v = (float)rel;
+        te.iv = __uint_as_float((uint32_t)(127 - rel) << 23);
       }
       put(k_s + s * kOp, kreg);
       fence_proxy_async_smem();
@@ -388,14 +436,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
         ok = false;
         break;
       }
-      {  // a block more than 2^64 below the largest counts as zero
-        const int j0 = kt.tile(i0 + j) * 128;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int blk = (j0 + (tid + 128 * i) / kPieces) >> 6;
-          if (blk < blocks && (int)__ldg(vx + blk) < evmax - 64) vreg[i] = make_uint4(0, 0, 0, 0);
-        }
-      }
+      for (int i = 0; i < kPieces; ++i)  // a block more than 2^64 below the largest counts as zero
+        if (far[i >= kPieces / 2]) vreg[i] = make_uint4(0, 0, 0, 0);
       put(v_s + s * kOp, vreg);
       fence_proxy_async_smem();
       mbar_arrive(&sh.v_full[s]);
@@ -410,49 +453,51 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
     setmaxnreg_dec<kRegsMma>();
     if (warp == 12 && elect_one() && n > 0) {
       constexpr uint32_t kIdesc = (1u << 4) | (8u << 24);  // FP32 accumulators, fp16 operands, M = 128
-      constexpr uint32_t kIdescS = kIdesc | (128u >> 3 << 17);
+      constexpr uint32_t kIdescS = kIdesc | (64u >> 3 << 17);
       constexpr uint32_t kIdescO = kIdesc | ((uint32_t)D >> 3 << 17) | (1u << 16);  // B: rows contracted
       const int tiles = two ? 2 : 1;
-      auto qk = [&](int t, int s) {
-        const uint64_t a = desc_sw128(q_s + t * kOp), bd = desc_sw128(k_s + s * kOp);
+      auto qk = [&](int t, int u) {  // scores of step u
+        const uint64_t a = desc_sw128(q_s + t * kOp);
+        const uint64_t bd = desc_sw128(k_s + ((u >> 1) & 1) * kOp) + (uint32_t)((u & 1) * (64 * 128 >> 4));
+        const uint32_t d = tmem + 128u * t + 64u * (u & 1);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (uint32_t)((k >> 2) * (kSlab >> 4) + (k & 3) * 2);
-          mma_ss(tmem + 128u * t, a + off, bd + off, kIdescS, k ? 1u : 0u);
+          mma_ss(d, a + off, bd + off, kIdescS, k ? 1u : 0u);
         }
+        mma_commit(&sh.s_full[t][u & 1]);
       };
       auto run = [&]() {
         if (!mbar_wait_bounded(&sh.q_full, 0u, abort, kWaitNs)) return false;
         if (!mbar_wait_bounded(&sh.k_full[0], 0u, abort, kWaitNs)) return false;
         tc_fence_after();
-        for (int t = 0; t < tiles; ++t) {
-          qk(t, 0);
-          mma_commit(&sh.s_full[t]);
-        }
+        for (int u = 0; u < 2; ++u)
+          for (int t = 0; t < tiles; ++t) qk(t, u);
         mma_commit(&sh.k_empty[0]);
-        for (int j = 0; j < n; ++j) {
-          const int s = j & 1, s1 = (j + 1) & 1;
-          for (int t = 0; t < tiles; ++t) {
-            if (t == 0 && !mbar_wait_bounded(&sh.v_full[s], (uint32_t)((j >> 1) & 1), abort, kWaitNs)) return false;
-            if (!mbar_wait_bounded(&sh.p_full[t], (uint32_t)(j & 1), abort, kWaitNs)) return false;
-            tc_fence_after();
-            const uint64_t vd = desc_mn_sw128(v_s + s * kOp);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_ts(tmem + 256u + (uint32_t)(D * t), tmem + 128u * t + 8u * k, vd + 128u * k, kIdescO,
-                     (j | k) ? 1u : 0u);
-            if (j + 1 < n) {
-              if (t == 0 && !mbar_wait_bounded(&sh.k_full[s1], (uint32_t)(((j + 1) >> 1) & 1), abort, kWaitNs))
-                return false;
-              tc_fence_after();
-              qk(t, s1);  // after the product before it, which reads the weights this overwrites
-              mma_commit(&sh.s_full[t]);
-            } else {
-              mma_commit(&sh.o_full[t]);
-            }
+        for (int u = 0; u < 2 * n; ++u) {
+          const int j = u >> 1, s = j & 1;
+          const bool more = u + 2 < 2 * n;
+          if ((u & 1) == 0) {
+            if (!mbar_wait_bounded(&sh.v_full[s], (uint32_t)((j >> 1) & 1), abort, kWaitNs)) return false;
+            if (more && !mbar_wait_bounded(&sh.k_full[s ^ 1], (uint32_t)(((j + 1) >> 1) & 1), abort, kWaitNs))
+              return false;
           }
-          mma_commit(&sh.v_empty[s]);
-          if (j + 1 < n) mma_commit(&sh.k_empty[s1]);
+          const uint64_t vd = desc_mn_sw128(v_s + s * kOp) + (uint32_t)((u & 1) * (64 * 128 >> 4));
+          for (int t = 0; t < tiles; ++t) {
+            if (!mbar_wait_bounded(&sh.p_full[t][u & 1], (uint32_t)((u >> 1) & 1), abort, kWaitNs)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ts(tmem + 256u + (uint32_t)(D * t), tmem + 128u * t + 64u * (u & 1) + 8u * k, vd + 128u * k, kIdescO,
+                     (u | k) ? 1u : 0u);
+            mma_commit(&sh.o_done[t]);
+            if (u + 1 == 2 * n) mma_commit(&sh.o_full[t]);
+            if (more) qk(t, u + 2);  // after the product before it, which reads the weights this overwrites
+          }
+          if (u & 1) {
+            mma_commit(&sh.v_empty[s]);
+            if (more) mma_commit(&sh.k_empty[s ^ 1]);
+          }
         }
         return true;
       };
