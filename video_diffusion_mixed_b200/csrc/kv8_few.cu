@@ -364,21 +364,20 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
   }
 }
 
-// Joins the parts of a row: out = sum 2^(lse_s - max) o_s / sum 2^(lse_s - max). A block per row; its
-// warps take the parts in turn, a lane D / 32 channels, and meet in shared memory in a fixed order. Parts
-// that saw no key have lse -inf.
-constexpr int kJoinWarps = 8;
-
-template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_kv8_join(const Kv8Attn p, int splits, float* part) {
-  __shared__ float sy[kJoinWarps][D], st[kJoinWarps];
+// Joins the parts of a row: out = sum 2^(lse_s - max) o_s / sum 2^(lse_s - max). W warps per row, eight a
+// block: they take the parts in turn, a lane D / 32 channels, and meet in shared memory in a fixed order.
+// Parts that saw no key have lse -inf. Eight warps for many parts (a token), one for many rows.
+template <int D, int W>
+__global__ void __launch_bounds__(256) k_kv8_join(const Kv8Attn p, int splits, float* part) {
+  __shared__ float sy[8][D], st[8];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (p.prec && *p.prec == SB_SKIP) return;
   constexpr int kE = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = (int)(p.heads_q / p.c.heads);
   const int64_t per = p.n_q * group;  // rows of a sequence and key head
-  const int64_t i = blockIdx.x;
+  const int64_t i = (int64_t)blockIdx.x * (8 / W) + warp / W;
+  if (i >= part_rows(p)) return;  // with W = 8 a block has one row
   const int64_t bh = i / per, r = i - bh * per, b = bh / p.c.heads, hk = bh - b * p.c.heads;
   const int64_t tok = r / group, hq = hk * group + r - tok * group;
   if (tok >= sequence_span(p, b).nq) return;
@@ -388,7 +387,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv8_join(const Kv8Attn p, i
   const float base = mx == -INFINITY ? 0.0f : mx;
   float tot = 0.0f, y[kE] = {};
 #pragma unroll 4
-  for (int s = warp; s < splits; s += kJoinWarps) {
+  for (int s = warp % W; s < splits; s += W) {
     const float f = fast_ex2(__ldcg(part_lse(p, part, splits, s, b, hk, r)) - base);
     const float* src = part_row(p, part, s, b, hk, r) + lane * kE;
     tot += f;
@@ -400,21 +399,31 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv8_join(const Kv8Attn p, i
       y[0] = fmaf(v.x, f, y[0]), y[1] = fmaf(v.y, f, y[1]);
     }
   }
+  if constexpr (W > 1) {
 #pragma unroll
-  for (int e = 0; e < kE; ++e) sy[warp][lane * kE + e] = y[e];
-  if (lane == 0) st[warp] = tot;
-  __syncthreads();
-  const int c = threadIdx.x * 2;  // two channels a thread
-  if (c >= D) return;
-  float t = 0.0f, a0 = 0.0f, a1 = 0.0f;
+    for (int e = 0; e < kE; ++e) sy[warp][lane * kE + e] = y[e];
+    if (lane == 0) st[warp] = tot;
+    __syncthreads();
+    if (warp != 0) return;
+    tot = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) t += st[w], a0 += sy[w][c], a1 += sy[w][c + 1];
-  const float inv = t > 0.0f ? 1.0f / t : t;
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + b * p.os[0] + tok * p.os[1] + hq * p.os[2] + c;
-  *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(__float_as_uint(a0 * inv), __float_as_uint(a1 * inv));
-  if (p.lse && c == 0)
+    for (int e = 0; e < kE; ++e) y[e] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      tot += st[w];
+#pragma unroll
+      for (int e = 0; e < kE; ++e) y[e] += sy[w][lane * kE + e];
+    }
+  }
+  const float inv = tot > 0.0f ? 1.0f / tot : tot;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + b * p.os[0] + tok * p.os[1] +
+                                              hq * p.os[2] + lane * kE);
+#pragma unroll
+  for (int c = 0; c < kE / 2; ++c)
+    dst[c] = pack_bf16x2(__float_as_uint(y[2 * c] * inv), __float_as_uint(y[2 * c + 1] * inv));
+  if (p.lse && lane == 0)
     p.lse[(b * p.heads_q + hq) * p.n_q + tok] =
-        t > 0.0f ? (mx + log2f(t)) * 0.6931471805599453f : t == 0.0f ? -INFINITY : t;
+        tot > 0.0f ? (mx + log2f(tot)) * 0.6931471805599453f : tot == 0.0f ? -INFINITY : tot;
 }
 
 static bool cache_map(CUtensorMap* m, const uint8_t* base, const sb_kv8& c) {
@@ -489,9 +498,14 @@ cudaError_t launch_kv8_attention(const Kv8Attn& p, void* part_, cudaStream_t s, 
   }
   if (e != cudaSuccess || splits == 1) return e;
   *why = "sb_kv8_attention (join)";
-  const LaunchAfter L((unsigned)part_rows(p), kJoinWarps * 32, 0, s, true);
-  return p.c.dim == 64 ? cudaLaunchKernelEx(&L.cfg, k_kv8_join<64>, p, splits, part)
-                       : cudaLaunchKernelEx(&L.cfg, k_kv8_join<128>, p, splits, part);
+  const int64_t all = part_rows(p);
+  const bool wide = splits > 16;
+  const LaunchAfter L((unsigned)(wide ? all : ceil_div(all, 8)), 256, 0, s, true);
+  if (p.c.dim == 64)
+    return wide ? cudaLaunchKernelEx(&L.cfg, k_kv8_join<64, 8>, p, splits, part)
+                : cudaLaunchKernelEx(&L.cfg, k_kv8_join<64, 1>, p, splits, part);
+  return wide ? cudaLaunchKernelEx(&L.cfg, k_kv8_join<128, 8>, p, splits, part)
+              : cudaLaunchKernelEx(&L.cfg, k_kv8_join<128, 1>, p, splits, part);
 }
 
 // The most that any number of key heads and any capacity need.

@@ -4,7 +4,7 @@
 // together (row = token * group + head in the group), so a key tile serves all of them. A CTA takes 256
 // rows (two tiles of 128, one warpgroup each) of one key head and a run of 128-token key tiles:
 //
-//   S = Q K^T       tcgen05 kind::f16, both operands in shared memory, FP32 in tensor memory
+//   S = Q K^T       tcgen05 kind::f16, Q (fp16) in tensor memory, K in shared memory, S (FP32) in tensor memory
 //   w = 2^(c S + ev - m), running maximum m and sum, one row a thread
 //   O += w V        tcgen05 kind::f16, w (fp16) from tensor memory, O (FP32) in tensor memory
 //
@@ -18,10 +18,11 @@
 // accumulator is rescaled rarely.
 //
 // Warps: 0-3 and 4-7 softmax of the two row tiles, 8-11 codes -> fp16, 12 MMA issue. A key tile is taken in
-// two steps of 64 keys (a scale block each). Each row tile has two 64-column score buffers, used in turn,
-// and the weights overwrite their scores: the scores of step u + 2 are computed as soon as the weights of
-// step u have been multiplied, so a softmax finds its next scores ready. Every wait is bounded
-// (SB_ETIMEOUT).
+// two steps of 64 keys (a scale block each); the weights overwrite their scores. The shared memory that
+// feeds the MMAs is the scarcest resource, so Q, which every step multiplies, lives in tensor memory. With
+// heads of 64 there is room for two score buffers a row tile, used in turn: the scores of step u + 2 are
+// computed as soon as the weights of step u have been multiplied, and a softmax finds its next scores
+// ready. With heads of 128 there is one. Every wait is bounded (SB_ETIMEOUT).
 #include "kv8.cuh"
 #include "launch_util.h"
 #include "sb_device.cuh"
@@ -56,7 +57,7 @@ struct TileShared {
 
 template <int D>
 constexpr int tile_smem() {
-  return 6 * (D / 64) * kSlab + (int)sizeof(TileShared) + 1024;
+  return 4 * (D / 64) * kSlab + (int)sizeof(TileShared) + 1024;
 }
 
 // B operand whose rows are the contraction axis (V: token rows of 64 channels): 128B swizzle, 8-token
@@ -71,14 +72,6 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr) {
   return d;
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -88,16 +81,23 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -143,9 +143,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
   if (p.prec && *p.prec == SB_SKIP) return;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   constexpr int kOp = (D / 64) * kSlab;  // one operand tile
-  TileShared& sh = *reinterpret_cast<TileShared*>(smem + 6 * kOp);
+  // tensor memory: score buffers of 64 columns, outputs, queries (fp16 pairs); 448 or 512 columns
+  constexpr int kBufs = D == 64 ? 2 : 1;
+  constexpr uint32_t kSCols = 64 * kBufs, kOCol = 2 * kSCols, kQCol = kOCol + 2 * D;
+  static_assert(kQCol + D <= 512, "tensor memory");
+  TileShared& sh = *reinterpret_cast<TileShared*>(smem + 4 * kOp);
   const uint32_t sbase = smem_u32(smem);
-  const uint32_t q_s = sbase, k_s = sbase + 2 * kOp, v_s = sbase + 4 * kOp;
+  const uint32_t k_s = sbase, v_s = sbase + 2 * kOp;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // this CTA's rows and key tiles
@@ -205,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
       const int64_t tok = live ? r / group : 0;
       const int64_t hq = hk * group + (live ? r - tok * group : 0);
       const int pos = sp.pos((int)tok);
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       float qc;
       {
         uint4 u[D / 8];
@@ -221,29 +226,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
         float f;
         qc = query_scale(p.scale, a, f);
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          float v[8];
-          unpack8(u[c], v);
-          st_shared_v4(tile_addr(q_s + t * kOp, row, c), pack_f16(v[0] * f, v[1] * f), pack_f16(v[2] * f, v[3] * f),
-                       pack_f16(v[4] * f, v[5] * f), pack_f16(v[6] * f, v[7] * f));
+        for (int h = 0; h < D / 32; ++h) {
+          uint32_t w[16];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float v[8];
+            unpack8(u[4 * h + c], v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[4 * c + i] = pack_f16(v[2 * i] * f, v[2 * i + 1] * f);
+          }
+          tmem_st16(tmem + lanes + kQCol + (uint32_t)(D / 2 * t) + 16u * h, w);
         }
-        fence_proxy_async_smem();
+        tmem_st_wait();
+        tc_fence_before();
         mbar_arrive(&sh.q_full);
       }
-      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t s_col = tmem + lanes + 128u * t, o_col = tmem + lanes + 256u + (uint32_t)(D * t);
+      const uint32_t s_col = tmem + lanes + kSCols * t, o_col = tmem + lanes + kOCol + (uint32_t)(D * t);
       float m = -INFINITY, l = 0.0f;
       bool ok = true;
       for (int u = 0; u < 2 * n; ++u) {
-        if (!mbar_wait_bounded(&sh.s_full[t][u & 1], (uint32_t)((u >> 1) & 1), abort, kWaitNs)) {
-          ok = false;
-          break;
-        }
+        const int buf = kBufs == 2 ? u & 1 : 0;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.s_full[t][buf], (uint32_t)((u / kBufs) & 1), abort, kWaitNs));
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t col = s_col + 64u * (u & 1);
-        uint32_t x[2][32];
-        tmem_ld32(col, x[0]);
-        tmem_ld32(col + 32u, x[1]);
+        const uint32_t col = s_col + 64u * buf;
+        uint32_t x[64];
+        tmem_ld64(col, x);
         const TileExp te = sh.exps[(u >> 1) & 3][u & 1];
         const float c = fminf(fmaxf(qc * te.k, 0x1p-126f), 0x1p126f);
         const int j0 = kt.tile(i0 + (u >> 1)) * 128 + (u & 1) * 64;
@@ -251,63 +259,57 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
         tmem_ld_wait();
         if (mask) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!key_visible(p, pos, j0 + 32 * h + i)) x[h][i] = 0xff800000u;
+          for (int i = 0; i < 64; ++i)
+            if (!key_visible(p, pos, j0 + i)) x[i] = 0xff800000u;
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]));
-        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-        const float mn = fmaxf(m, fmaf(top, c, te.v));
+        for (int i = 0; i < 64; i += 2)
+          mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+        const float mn = fmaxf(m, fmaf(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), c, te.v));
         if (__any_sync(0xffffffffu, mn > m + kRise)) {
           const float f = mn == m ? 1.0f : ex2(m - mn);
           m = mn;
           l *= f;
-          if (u > 0) {
-            ok = mbar_wait_bounded(&sh.o_done[t], (uint32_t)((u - 1) & 1), abort, kWaitNs);
-            if (!__all_sync(0xffffffffu, ok)) {
-              ok = false;
-              break;
-            }
+          if (u > 0) {  // the accumulator is complete up to step u - 1 once that step's product is done; the
+                        // phase before is behind the scores just read, so the parity is not ambiguous
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.o_done[t], (uint32_t)((u - 1) & 1), abort, kWaitNs));
+            if (!ok) break;
             tc_fence_after();
-#pragma unroll
-            for (int h = 0; h < D / 32; ++h) {
-              uint32_t o[32];
-              tmem_ld32(o_col + 32u * h, o);
+#pragma unroll 1
+            for (int h = 0; h < D / 16; ++h) {
+              uint32_t o[16];
+              tmem_ld16(o_col + 16u * h, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st32(o_col + 32u * h, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st16(o_col + 16u * h, o);
             }
           }
         }
         const float add = te.v - (m == -INFINITY ? 0.0f : m);
         const uint64_t cc = pack2(c, c), aa = pack2(add, add);
         uint64_t sum[2] = {0, 0};
-        uint32_t w[32];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             float y0, y1;
-            unpack2(fma2(pack2u(x[h][i], x[h][i + 1]), cc, aa), y0, y1);
+            unpack2(fma2(pack2u(x[32 * h + i], x[32 * h + i + 1]), cc, aa), y0, y1);
             y0 = ex2(y0);
             y1 = ex2(y1);
             sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(y0, y1));
-            w[16 * h + i / 2] = pack_f16(y0, y1);
+            w[i / 2] = pack_f16(y0, y1);
           }
-        tmem_st32(col, w);
+          tmem_st16(col + 16u * h, w);
+        }
         float s0, s1;
         unpack2(add2(sum[0], sum[1]), s0, s1);
         l = fmaf(s0 + s1, te.iv, l);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&sh.p_full[t][u & 1]);
+        mbar_arrive(&sh.p_full[t][buf]);
       }
       if (ok && n > 0) ok = mbar_wait_bounded(&sh.o_full[t], 0u, abort, kWaitNs);
       if (!ok) {
@@ -457,47 +459,45 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
       constexpr uint32_t kIdescO = kIdesc | ((uint32_t)D >> 3 << 17) | (1u << 16);  // B: rows contracted
       const int tiles = two ? 2 : 1;
       auto qk = [&](int t, int u) {  // scores of step u
-        const uint64_t a = desc_sw128(q_s + t * kOp);
         const uint64_t bd = desc_sw128(k_s + ((u >> 1) & 1) * kOp) + (uint32_t)((u & 1) * (64 * 128 >> 4));
-        const uint32_t d = tmem + 128u * t + 64u * (u & 1);
+        const int buf = kBufs == 2 ? u & 1 : 0;
+        const uint32_t d = tmem + kSCols * t + 64u * buf, a = tmem + kQCol + (uint32_t)(D / 2 * t);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (uint32_t)((k >> 2) * (kSlab >> 4) + (k & 3) * 2);
-          mma_ss(d, a + off, bd + off, kIdescS, k ? 1u : 0u);
+          mma_ts(d, a + 8u * k, bd + off, kIdescS, k ? 1u : 0u);
         }
-        mma_commit(&sh.s_full[t][u & 1]);
+        mma_commit(&sh.s_full[t][buf]);
       };
       auto run = [&]() {
         if (!mbar_wait_bounded(&sh.q_full, 0u, abort, kWaitNs)) return false;
         if (!mbar_wait_bounded(&sh.k_full[0], 0u, abort, kWaitNs)) return false;
         tc_fence_after();
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < kBufs; ++u)
           for (int t = 0; t < tiles; ++t) qk(t, u);
-        mma_commit(&sh.k_empty[0]);
+        if (kBufs == 2) mma_commit(&sh.k_empty[0]);
         for (int u = 0; u < 2 * n; ++u) {
-          const int j = u >> 1, s = j & 1;
-          const bool more = u + 2 < 2 * n;
-          if ((u & 1) == 0) {
-            if (!mbar_wait_bounded(&sh.v_full[s], (uint32_t)((j >> 1) & 1), abort, kWaitNs)) return false;
-            if (more && !mbar_wait_bounded(&sh.k_full[s ^ 1], (uint32_t)(((j + 1) >> 1) & 1), abort, kWaitNs))
-              return false;
-          }
+          const int j = u >> 1, s = j & 1, v = u + kBufs;  // v: the step whose scores take this one's place
+          const bool more = v < 2 * n;
+          if ((u & 1) == 0 && !mbar_wait_bounded(&sh.v_full[s], (uint32_t)((j >> 1) & 1), abort, kWaitNs)) return false;
+          if ((v & 1) == 0 && more &&
+              !mbar_wait_bounded(&sh.k_full[(v >> 1) & 1], (uint32_t)((v >> 2) & 1), abort, kWaitNs))
+            return false;
+          const int buf = kBufs == 2 ? u & 1 : 0;
           const uint64_t vd = desc_mn_sw128(v_s + s * kOp) + (uint32_t)((u & 1) * (64 * 128 >> 4));
           for (int t = 0; t < tiles; ++t) {
-            if (!mbar_wait_bounded(&sh.p_full[t][u & 1], (uint32_t)((u >> 1) & 1), abort, kWaitNs)) return false;
+            if (!mbar_wait_bounded(&sh.p_full[t][buf], (uint32_t)((u / kBufs) & 1), abort, kWaitNs)) return false;
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_ts(tmem + 256u + (uint32_t)(D * t), tmem + 128u * t + 64u * (u & 1) + 8u * k, vd + 128u * k, kIdescO,
+              mma_ts(tmem + kOCol + (uint32_t)(D * t), tmem + kSCols * t + 64u * buf + 8u * k, vd + 128u * k, kIdescO,
                      (u | k) ? 1u : 0u);
             mma_commit(&sh.o_done[t]);
             if (u + 1 == 2 * n) mma_commit(&sh.o_full[t]);
-            if (more) qk(t, u + 2);  // after the product before it, which reads the weights this overwrites
+            if (more) qk(t, v);  // after the product before it, which reads the weights this overwrites
           }
-          if (u & 1) {
-            mma_commit(&sh.v_empty[s]);
-            if (more) mma_commit(&sh.k_empty[s ^ 1]);
-          }
+          if (u & 1) mma_commit(&sh.v_empty[s]);
+          if (more && (v & 1)) mma_commit(&sh.k_empty[(v >> 1) & 1]);
         }
         return true;
       };
