@@ -10,6 +10,7 @@ caller-owned device buffers with torch; the library itself never allocates.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -533,25 +534,36 @@ def _need(cond: bool, status: int, msg: str):
         raise SixbitError(status, msg)
 
 
-def _dev(device, *tensors):
-    """The tensors are CUDA tensors of one device, and it is the current one (kernels launch there)."""
+def _dev(device: int, *tensors):
+    """The tensors are on CUDA device `device`, and it is the current one (kernels launch there)."""
     for t in tensors:
-        if t is not None:
-            _need(t.is_cuda, SB_EINVAL, "a tensor is not on a CUDA device")
-            _need(t.device == device, SB_EINVAL, f"a tensor is on {t.device}, another on {device}")
-    _need(device.index == torch.cuda.current_device(), SB_EINVAL,
-          f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+        if t is not None and t.get_device() != device:
+            raise SixbitError(SB_EINVAL, f"a tensor is on {t.device}, expected cuda:{device}")
+    if device < 0:
+        raise SixbitError(SB_EINVAL, "the tensors are not on a CUDA device")
+    if device != torch.cuda.current_device():
+        raise SixbitError(SB_EINVAL, f"the tensors are on cuda:{device}, the current device is "
+                          f"cuda:{torch.cuda.current_device()}")
 
 
 def _typed(t, dtype, shape, name: str):
-    if t is not None:
-        _need(t.dtype == dtype, SB_EINVAL, f"{name} must be {dtype}, not {t.dtype}")
-        _need(tuple(t.shape) == tuple(shape), SB_ESHAPE, f"{name} is {tuple(t.shape)}, expected {tuple(shape)}")
-        _need(t.is_contiguous(), SB_EINVAL, f"{name} must be contiguous")
+    """A contiguous tensor of this type and shape, or None."""
+    if t is None:
+        return
+    if t.dtype is not dtype:
+        raise SixbitError(SB_EINVAL, f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise SixbitError(SB_ESHAPE, f"{name} is {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise SixbitError(SB_EINVAL, f"{name} must be contiguous")
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
 
 
 class Fp8Tensor:
@@ -562,6 +574,7 @@ class Fp8Tensor:
         self.codes = torch.empty((rows, cols), dtype=torch.uint8, device=device)
         self.sf = torch.empty(int(lib().sb_fp8_sf_bytes(rows, cols)), dtype=torch.uint8, device=device)
         self._c = Fp8(self.codes.data_ptr(), self.sf.data_ptr(), rows, cols)
+        self._ref = ctypes.byref(self._c)
 
     def c(self) -> Fp8:
         return self._c
@@ -578,12 +591,13 @@ class WeightFp8:
 
     def __init__(self, W: torch.Tensor, bias: torch.Tensor | None = None, ws: Workspace | None = None, stream=None):
         N, K = W.shape
-        _dev(W.device, W, bias)
+        _dev(W.get_device(), bias)
         _typed(W, torch.bfloat16, (N, K), "W")
         _typed(bias, torch.bfloat16, (N,), "bias")
         self.N, self.K, self.bias = N, K, bias
         self.w = Fp8Tensor(N, K, W.device)
         self._c = WeightFp8C()
+        self._ref = ctypes.byref(self._c)
         self._c.w = self.w.c()
         ws = ws or Workspace(1, 1, W.device, stream)
         _ck(lib().sb_prepare_weight_fp8(_ptr(W), _ptr(bias), N, K, ctypes.byref(self._c), ws.ptr, _stream(stream)))
@@ -595,7 +609,7 @@ class WeightFp8:
 def fp8_encode(X, a: Fp8Tensor, ws: Workspace, prec=None, stream=None):
     """sb_fp8_encode: the codes and scales of X [M, K] bf16 into a."""
     M, K = X.shape
-    _dev(X.device, X, a.codes, prec)
+    _dev(X.get_device(), a.codes, prec)
     _typed(X, torch.bfloat16, (M, K), "X")
     _ck(lib().sb_fp8_encode(_ptr(X), M, K, _ptr(prec), ctypes.byref(a.c()), ws.ptr, _stream(stream)))
 
@@ -606,13 +620,12 @@ def linear_fp8(X, a: Fp8Tensor, w: WeightFp8, Y, epilogue: int = EPI_NONE, prec=
     output type is Y's (bf16 or float32)."""
     M = a.rows
     _need(ws is not None, SB_EINVAL, "ws is required")
-    _dev(Y.device, Y, X, a.codes, w.w.codes, prec)
+    _dev(Y.get_device(), X, a.codes, w.w.codes, prec, ws.buf)
     _typed(X, torch.bfloat16, (M, w.K), "X")
-    _need(Y.dtype in (torch.bfloat16, torch.float32), SB_EINVAL, f"Y must be bfloat16 or float32, not {Y.dtype}")
-    _typed(Y, Y.dtype, (M, w.N), "Y")
-    out = OUT_F32 if Y.dtype == torch.float32 else OUT_BF16
-    _ck(lib().sb_linear_fp8(_ptr(X), ctypes.byref(a.c()), _ptr(prec), ctypes.byref(w.c()), epilogue, out, _ptr(Y), M,
-                            ws.ptr, _stream(stream)))
+    f32 = Y.dtype is torch.float32
+    _typed(Y, torch.float32 if f32 else torch.bfloat16, (M, w.N), "Y")
+    _ck(lib().sb_linear_fp8(_ptr(X), a._ref, _ptr(prec), w._ref, epilogue, OUT_F32 if f32 else OUT_BF16, Y.data_ptr(),
+                            M, ws.buf.data_ptr(), _raw_stream(stream)))
 
 
 class KvCache8:
@@ -634,11 +647,13 @@ class KvCache8:
         for t, name in ((self.k_exp, "k_exp"), (self.v_exp, "v_exp")):
             _typed(t, torch.uint8, (batch, heads, capacity // 64), name)
         _typed(self.lens, torch.int32, (batch,), "lens")
-        self.device = self.k_codes.device
+        self.device = self.k_codes.get_device()
         for t in buffers:
-            _need(t.is_cuda and t.device == self.device, SB_EINVAL, "the cache's buffers must be on one CUDA device")
+            _need(t.is_cuda and t.get_device() == self.device, SB_EINVAL,
+                  "the cache's buffers must be on one CUDA device")
         self._c = Kv8(self.k_codes.data_ptr(), self.v_codes.data_ptr(), self.k_exp.data_ptr(), self.v_exp.data_ptr(),
                       self.lens.data_ptr(), batch, heads, capacity, dim)
+        self._ref = ctypes.byref(self._c)
 
     def c(self) -> Kv8:
         return self._c
@@ -659,43 +674,53 @@ class AttnWorkspace:
         return _p(self.buf)
 
 
+@functools.lru_cache(maxsize=256)
+def _stride_array(sb: int, st: int, sh: int):
+    return (ctypes.c_int64 * 3)(sb, st, sh)
+
+
 def _strides(t, name: str):
     """(batch, token, head) strides of a [B, T, H, D] bf16 tensor whose channels are contiguous (0 for
     an axis of one)."""
-    _need(t.dtype == torch.bfloat16, SB_EINVAL, f"{name} must be torch.bfloat16, not {t.dtype}")
-    _need(t.stride(3) == 1, SB_EINVAL, f"{name}: the channels of a head must be contiguous")
-    return (ctypes.c_int64 * 3)(*(0 if n == 1 else s for n, s in zip(t.shape[:3], t.stride())))
+    if t.dtype is not torch.bfloat16:
+        raise SixbitError(SB_EINVAL, f"{name} must be torch.bfloat16, not {t.dtype}")
+    sb, st, sh, sd = t.stride()
+    if sd != 1:
+        raise SixbitError(SB_EINVAL, f"{name}: the channels of a head must be contiguous")
+    B, T, H, _ = t.shape
+    return _stride_array(sb if B > 1 else 0, st if T > 1 else 0, sh if H > 1 else 0)
 
 
 def kv8_store(k, v, cache: KvCache8, start=None, counts=None, prec=None, ws=None, stream=None):
     """sb_kv8_store: keys and values [B, n, H, D] bf16 (any strides with contiguous channels) into the
     cache at positions start[b] (None: behind the tokens held); counts[b] of the n rows (None: all)."""
-    n = k.shape[1]
     _need(ws is not None, SB_EINVAL, "ws is required")
-    _dev(cache.device, k, v, start, counts, prec)
-    for t, name in ((k, "k"), (v, "v")):
-        _need(tuple(t.shape) == (cache.batch, n, cache.heads, cache.dim), SB_ESHAPE,
-              f"{name} is {tuple(t.shape)}, expected {(cache.batch, n, cache.heads, cache.dim)}")
+    _need(k.dim() == 4, SB_ESHAPE, f"k is {tuple(k.shape)}, expected [B, n, H, D]")
+    shape = (cache.batch, k.shape[1], cache.heads, cache.dim)
+    _dev(cache.device, k, v, start, counts, prec, ws.buf)
+    if k.shape != shape or v.shape != shape:
+        raise SixbitError(SB_ESHAPE, f"k is {tuple(k.shape)}, v {tuple(v.shape)}, expected {shape}")
     _typed(start, torch.int32, (cache.batch,), "start")
     _typed(counts, torch.int32, (cache.batch,), "counts")
-    _ck(lib().sb_kv8_store(_ptr(k), _strides(k, "k"), _ptr(v), _strides(v, "v"), n, ctypes.byref(cache.c()),
-                           _ptr(start), _ptr(counts), _ptr(prec), ws.ptr, _stream(stream)))
+    _ck(lib().sb_kv8_store(k.data_ptr(), _strides(k, "k"), v.data_ptr(), _strides(v, "v"), shape[1], cache._ref,
+                           _ptr(start), _ptr(counts), _ptr(prec), ws.buf.data_ptr(), _raw_stream(stream)))
 
 
 def kv8_attention(q, cache: KvCache8, out, lse=None, scale: float | None = None, causal: bool = False,
                   window: int = 0, sinks: int = 0, q_lens=None, prec=None, ws: AttnWorkspace = None, stream=None):
     """sb_kv8_attention: out [B, n, Hq, D] = softmax(scale q k^T) v over the cache; scale None is
     1 / sqrt(D); lse: float32 [B, Hq, n] or None."""
-    B, n, Hq, D = q.shape
     _need(ws is not None, SB_EINVAL, "ws is required")
-    _dev(cache.device, q, out, lse, q_lens, prec)
-    _need((B, D) == (cache.batch, cache.dim), SB_ESHAPE, f"q is {tuple(q.shape)}, the cache holds {cache.batch} "
-          f"sequences of heads of {cache.dim}")
-    _need(out.shape == q.shape, SB_ESHAPE, f"out is {tuple(out.shape)}, expected {tuple(q.shape)}")
+    _need(q.dim() == 4, SB_ESHAPE, f"q is {tuple(q.shape)}, expected [B, n, Hq, D]")
+    B, n, Hq, D = q.shape
+    _dev(cache.device, q, out, lse, q_lens, prec, ws.buf)
+    if B != cache.batch or D != cache.dim or out.shape != q.shape:
+        raise SixbitError(SB_ESHAPE, f"q is {tuple(q.shape)}, out {tuple(out.shape)}, the cache holds {cache.batch} "
+                          f"sequences of heads of {cache.dim}")
     _need(all(m == 1 or s > 0 for m, s in zip(out.shape, out.stride())), SB_EINVAL, "out must not be broadcast")
     _typed(lse, torch.float32, (B, Hq, n), "lse")
     _typed(q_lens, torch.int32, (B,), "q_lens")
-    opt = Attn(1.0 / D ** 0.5 if scale is None else scale, int(causal), window, sinks)
-    _ck(lib().sb_kv8_attention(_ptr(q), _strides(q, "q"), n, Hq, ctypes.byref(cache.c()), ctypes.byref(opt),
-                               _ptr(q_lens), _ptr(out), _strides(out, "out"), _ptr(lse), _ptr(prec), ws.ptr,
-                               ws.bytes, _stream(stream)))
+    opt = Attn(D ** -0.5 if scale is None else scale, bool(causal), window, sinks)
+    _ck(lib().sb_kv8_attention(q.data_ptr(), _strides(q, "q"), n, Hq, cache._ref, ctypes.byref(opt), _ptr(q_lens),
+                               out.data_ptr(), _strides(out, "out"), _ptr(lse), _ptr(prec), ws.buf.data_ptr(),
+                               ws.bytes, _raw_stream(stream)))
