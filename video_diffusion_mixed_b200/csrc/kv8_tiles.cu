@@ -364,18 +364,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
     const uint8_t* kx = p.c.k_exp + head0 / 64;
     const uint8_t* vx = p.c.v_exp + head0 / 64;
     const int blocks = (sp.len + 63) >> 6;
-    {  // the largest exponent of V over this CTA's tiles
-      int e = 0;
-      for (int i = tid; i < 2 * n; i += 128) {
-        const int blk = kt.tile(i0 + (i >> 1)) * 2 + (i & 1);
-        if (blk < blocks) e = max(e, (int)vx[blk]);
-      }
-#pragma unroll
-      for (int s = 16; s >= 1; s >>= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, s));
-      if (lane == 0) atomicMax(&sh.evmax, e);
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-    }
-    const int evmax = sh.evmax;
     uint4 kreg[kPieces], vreg[kPieces];
     int ke[2] = {127, 127}, ve[2] = {0, 0};  // exponent bytes of the next tile's blocks
     auto fetch = [&](const uint8_t* codes, int j, uint4 (&u)[kPieces]) {
@@ -412,6 +400,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
       fetch_exps(0);
       fetch(p.c.v_codes, 0, vreg);
     }
+    {  // the largest exponent of V over this CTA's tiles
+      int e = 0;
+      for (int i = tid; i < 2 * n; i += 128) {
+        const int blk = kt.tile(i0 + (i >> 1)) * 2 + (i & 1);
+        if (blk < blocks) e = max(e, (int)vx[blk]);
+      }
+#pragma unroll
+      for (int s = 16; s >= 1; s >>= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, s));
+      if (lane == 0) atomicMax(&sh.evmax, e);
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+    }
+    const int evmax = sh.evmax;
     for (int j = 0; ok && j < n; ++j) {
       const int s = j & 1;
       const uint32_t ph = (uint32_t)((j >> 1) & 1);
