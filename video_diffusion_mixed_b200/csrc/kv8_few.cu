@@ -1,9 +1,11 @@
 // kv8_few.cu -- attention over the FP8 key/value cache for few query rows (at most 16 for a key head:
 // the tokens being generated), and the join of partial results.
 //
-// Bound by reading the visible part of the cache once (2 D bytes a token and head), so the keys are
-// split over many blocks, and each warp streams 32-token steps of its block's share on its own: one TMA
-// box of keys and one of values a step, three steps deep, no barrier between warps before the end.
+// Bound by reading the visible part of the cache once (2 D bytes a token and head). The 64-token tiles of
+// all sequences and key heads, one after the other, are dealt out evenly to one wave of blocks, whatever
+// the lengths: a block's share may end in the middle of a head (the parts are joined afterwards) and hold
+// several heads. Within a share of a head each warp streams 32-token steps on its own: one TMA box of keys
+// and one of values a step, three steps deep, no barrier between warps before the end.
 // The products run on 16 x 8 matrix instructions in fp16 (codes are exact there) with FP32 sums, with the
 // cache on the side of 16 and the query rows on the side of 8, so that few rows waste little:
 //
@@ -61,14 +63,73 @@ __device__ __forceinline__ uint32_t box_addr(uint32_t box, int r, int c) {
   return box + (uint32_t)(r * D + (((c >> 4) ^ x) << 4) + (c & 15));
 }
 
+// The tiles of one sequence's key head: at least one, which shows a query that it sees nothing.
+__device__ __forceinline__ int few_tiles(const Kv8Attn& p, const Span& sp) {
+  if (sp.nq == 0) return 0;
+  return max(1, key_tiles(p, sp.pos(0), sp.pos(sp.nq - 1), 64).n);
+}
+
+// A place in the row of all tiles (sequence after sequence, key head after key head).
+struct FewPlace {
+  int64_t total;  // tiles of all
+  int64_t before; // tiles before sequence b
+  int b, n;       // the sequence, and the tiles of one of its key heads
+};
+// Whole warps: the place of tile t, or of sequence `seq` where seq >= 0. Reads every length (the host
+// takes this path for at most kFewUnits sequences).
+__device__ __forceinline__ FewPlace few_place(const Kv8Attn& p, int64_t t, int seq, int lane, bool report) {
+  FewPlace f{0, 0, -1, 0};
+  for (int64_t b0 = 0; b0 < p.c.batch; b0 += 32) {
+    const int64_t b = b0 + lane;
+    int n = 0;
+    if (b < p.c.batch) {
+      const Span sp = sequence_span(p, b);
+      if (report && sp.bad) set_error(p.hdr, SB_ESHAPE);
+      n = few_tiles(p, sp);
+    }
+    int64_t sum = n;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, sum, s);
+      if (lane >= s) sum += v;
+    }
+    const int64_t end = f.total + sum * p.c.heads, start = end - (int64_t)n * p.c.heads;
+    const bool here = seq >= 0 ? b == seq : n > 0 && t >= start && t < end;
+    const unsigned hit = __ballot_sync(0xffffffffu, here);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      f.b = (int)b0 + src;
+      f.n = __shfl_sync(0xffffffffu, n, src);
+      f.before = __shfl_sync(0xffffffffu, start, src);
+    }
+    f.total = __shfl_sync(0xffffffffu, end, 31);
+  }
+  return f;
+}
+// Blocks that get a share: at least four tiles each. Block c has the tiles [c total / shares, (c + 1) total /
+// shares); tile t belongs to the largest c with c total / shares <= t.
+__device__ __forceinline__ int64_t few_shares(int64_t total, int blocks) {
+  return max((int64_t)1, min((int64_t)blocks, (total + 3) / 4));
+}
+__device__ __forceinline__ int64_t few_owner(int64_t t, int64_t total, int64_t shares) {
+  return ((t + 1) * shares - 1) / total;
+}
+// Partial results: a block has at most two, of the head that it takes over and of the one it hands on.
+__device__ __forceinline__ float* few_part(float* part, int D, int64_t block, int side, int r) {
+  return part + ((block * 2 + side) * kFewRows + r) * D;
+}
+__device__ __forceinline__ float* few_part_lse(float* part, int D, int blocks, int64_t block, int side, int r) {
+  return part + (int64_t)blocks * 2 * kFewRows * D + (block * 2 + side) * kFewRows + r;
+}
+
 template <int D>
 constexpr int few_smem() {
   return kFewWarps * kFewSlots * 2 * kStep * D + 1024 + kFewWarps * kFewSlots * 8;
 }
 
-// NT tiles of eight query rows.
+// NT tiles of eight query rows. deal: the tiles are dealt out as above; otherwise a block takes one head.
 template <int D, int NT>
-__global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__ FewMaps tm, const Kv8Attn p, int splits,
+__global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__ FewMaps tm, const Kv8Attn p, int deal,
                                                          float* part) {
   extern __shared__ uint8_t few_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(few_smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -76,354 +137,434 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
   if (p.prec && *p.prec == SB_SKIP) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int group = (int)(p.heads_q / p.c.heads);
-  const int split = blockIdx.x;
-  const int64_t hk = blockIdx.y, b = blockIdx.z;
-  const Span sp = sequence_span(p, b);
-  if (split == 0 && hk == 0 && tid == 0 && sp.bad) set_error(p.hdr, SB_ESHAPE);
-  const int rows = sp.nq * group;
-  if (rows == 0) return;
-  const int pmin = sp.pos(0), pmax = sp.pos(sp.nq - 1);
-  const KeyTiles kt = key_tiles(p, pmin, pmax, 64);
-  const int i0 = (int)((int64_t)kt.n * split / splits), i1 = (int)((int64_t)kt.n * (split + 1) / splits);
-  const int steps = 2 * (i1 - i0);
-  const int head = (int)(b * p.c.heads + hk);
-  const uint8_t* kx = p.c.k_exp + (int64_t)head * (p.c.capacity / 64);
-  const uint8_t* vx = p.c.v_exp + (int64_t)head * (p.c.capacity / 64);
+  int64_t at = 0, at_end = 0;
+  if (deal) {
+    const FewPlace f = few_place(p, -1, -1, lane, blockIdx.x == 0 && warp == 0);
+    const int64_t shares = few_shares(f.total, gridDim.x);
+    if (blockIdx.x >= shares) return;
+    at = blockIdx.x * f.total / shares;
+    at_end = (blockIdx.x + 1) * f.total / shares;
+    if (at >= at_end) return;
+  }
 
   // this warp's ring: slot s holds a box of keys, then one of values
   const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kFewSlots * 2 * kBox);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kFewWarps * kFewSlots * 2 * kBox) + warp * kFewSlots;
-  auto fetch = [&](int slot, int q) {  // one lane
-    if (q >= steps) return;
-    const int j0 = kt.tile(i0 + (q >> 1)) * 64 + (q & 1) * kStep;
-    const uint32_t box = ring + (uint32_t)(slot * 2 * kBox), bar = smem_u32(&full[slot]);
-    mbar_arrive_expect_tx(&full[slot], 2 * kBox);
-    tma_load_3d(box, &tm.k, bar, 0, j0, head);
-    tma_load_3d(box + kBox, &tm.v, bar, 0, j0, head);
-  };
   if (lane == 0) {
     for (int u = 0; u < kFewSlots; ++u) mbar_init(&full[u], 1);
     fence_barrier_init();
     fence_proxy_async_smem();
-    for (int u = 0; u < kFewSlots; ++u) fetch(u, warp + u * kFewWarps);
   }
   __syncwarp();
+  int slot = 0;  // the ring goes on from head to head
+  uint32_t ph = 0;
+  bool late = false;
 
-  // queries as the right operand: row 8n + g, channels 64c + 16t + 4i .. + 3
-  uint32_t qf[NT][kC][4][2];
-  float qc[NT][2];  // rows 8n + 2t, 8n + 2t + 1
-  int pos[NT][2];
+  while (true) {
+    // this head's share: tiles i0 .. i1 - 1 of its `tiles`
+    int64_t hk, b;
+    int i0, i1, tiles;
+    if (deal) {
+      const FewPlace f = few_place(p, at, -1, lane, false);
+      const int64_t in = at - f.before;
+      b = f.b;
+      tiles = f.n;
+      hk = in / tiles;
+      i0 = (int)(in - hk * tiles);
+      i1 = (int)min((int64_t)tiles, i0 + (at_end - at));
+    } else {
+      b = blockIdx.x / p.c.heads;
+      hk = blockIdx.x - b * p.c.heads;
+      const Span sp = sequence_span(p, b);
+      if (hk == 0 && tid == 0 && sp.bad) set_error(p.hdr, SB_ESHAPE);
+      tiles = few_tiles(p, sp);
+      if (tiles == 0) return;
+      i0 = 0;
+      i1 = tiles;
+    }
+    const Span sp = sequence_span(p, b);
+    const int rows = sp.nq * group;
+    const int pmin = sp.pos(0), pmax = sp.pos(sp.nq - 1);
+    const KeyTiles kt = key_tiles(p, pmin, pmax, 64);  // none: tile 0, where every key is masked
+    const int steps = 2 * (i1 - i0);
+    const int head = (int)(b * p.c.heads + hk);
+    const uint8_t* kx = p.c.k_exp + (int64_t)head * (p.c.capacity / 64);
+    const uint8_t* vx = p.c.v_exp + (int64_t)head * (p.c.capacity / 64);
+    auto fetch = [&](int into, int q) {  // one lane
+      if (q >= steps) return;
+      const int j0 = kt.tile(i0 + (q >> 1)) * 64 + (q & 1) * kStep;
+      const uint32_t box = ring + (uint32_t)(into * 2 * kBox), bar = smem_u32(&full[into]);
+      mbar_arrive_expect_tx(&full[into], 2 * kBox);
+      tma_load_3d(box, &tm.k, bar, 0, j0, head);
+      tma_load_3d(box + kBox, &tm.v, bar, 0, j0, head);
+    };
+    if (lane == 0) {
+      for (int u = 0; u < kFewSlots; ++u) fetch((slot + u) % kFewSlots, warp + u * kFewWarps);
+    }
+    __syncwarp();
+
+    // queries as the right operand: row 8n + g, channels 64c + 16t + 4i .. + 3
+    uint32_t qf[NT][kC][4][2];
+    float qc[NT][2];  // rows 8n + 2t, 8n + 2t + 1
+    int pos[NT][2];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int r = g + 8 * n;
-    const bool live = r < rows;
-    const int tok = live ? r / group : 0;
-    const int64_t hq = hk * group + (live ? r - tok * group : 0);
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + b * p.qs[0] + tok * p.qs[1] + hq * p.qs[2];
-    uint4 u[kC][2];
-    uint32_t a = 0;
+    for (int n = 0; n < NT; ++n) {
+      const int r = g + 8 * n;
+      const bool live = r < rows;
+      const int tok = live ? r / group : 0;
+      const int64_t hq = hk * group + (live ? r - tok * group : 0);
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + b * p.qs[0] + tok * p.qs[1] + hq * p.qs[2];
+      uint4 u[kC][2];
+      uint32_t a = 0;
 #pragma unroll
-    for (int c = 0; c < kC; ++c) {
+      for (int c = 0; c < kC; ++c) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        u[c][i] = live ? __ldg(reinterpret_cast<const uint4*>(q + 64 * c + 16 * t) + i) : make_uint4(0, 0, 0, 0);
-        a = __vmaxu2(a, __vmaxu2(__vmaxu2(u[c][i].x & 0x7fff7fffu, u[c][i].y & 0x7fff7fffu),
-                                 __vmaxu2(u[c][i].z & 0x7fff7fffu, u[c][i].w & 0x7fff7fffu)));
+        for (int i = 0; i < 2; ++i) {
+          u[c][i] = live ? __ldg(reinterpret_cast<const uint4*>(q + 64 * c + 16 * t) + i) : make_uint4(0, 0, 0, 0);
+          a = __vmaxu2(a, __vmaxu2(__vmaxu2(u[c][i].x & 0x7fff7fffu, u[c][i].y & 0x7fff7fffu),
+                                   __vmaxu2(u[c][i].z & 0x7fff7fffu, u[c][i].w & 0x7fff7fffu)));
+        }
+      }
+      a = max(a & 0xffffu, a >> 16);
+      a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+      a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+      float f;
+      const float back = query_scale(p.scale, a, f);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int rr = 8 * n + 2 * t + e;
+        qc[n][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + e));
+        pos[n][e] = rr < rows ? sp.pos(rr / group) : -1;
+      }
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float v[8];
+          unpack8(u[c][i], v);
+          qf[n][c][2 * i][0] = pack_f16(v[0] * f, v[1] * f);
+          qf[n][c][2 * i][1] = pack_f16(v[2] * f, v[3] * f);
+          qf[n][c][2 * i + 1][0] = pack_f16(v[4] * f, v[5] * f);
+          qf[n][c][2 * i + 1][1] = pack_f16(v[6] * f, v[7] * f);
+        }
       }
     }
-    a = max(a & 0xffffu, a >> 16);
-    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-    float f;
-    const float back = query_scale(p.scale, a, f);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int rr = 8 * n + 2 * t + e;
-      qc[n][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + e));
-      pos[n][e] = rr < rows ? sp.pos(rr / group) : -1;
+    // the largest exponent of V over the block's share (while the first boxes are on their way)
+    const int blocks = (sp.len + 63) >> 6;
+    int evmax = 0;
+    for (int i = lane; i < i1 - i0; i += 32) {
+      const int blk = kt.tile(i0 + i);
+      if (blk < blocks) evmax = max(evmax, (int)__ldg(vx + blk));
     }
 #pragma unroll
-    for (int c = 0; c < kC; ++c) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float v[8];
-        unpack8(u[c][i], v);
-        qf[n][c][2 * i][0] = pack_f16(v[0] * f, v[1] * f);
-        qf[n][c][2 * i][1] = pack_f16(v[2] * f, v[3] * f);
-        qf[n][c][2 * i + 1][0] = pack_f16(v[4] * f, v[5] * f);
-        qf[n][c][2 * i + 1][1] = pack_f16(v[6] * f, v[7] * f);
-      }
-    }
-  }
-  // the largest exponent of V over the block's share (while the first boxes are on their way)
-  const int blocks = (sp.len + 63) >> 6;
-  int evmax = 0;
-  for (int i = lane; i < i1 - i0; i += 32) {
-    const int blk = kt.tile(i0 + i);
-    if (blk < blocks) evmax = max(evmax, (int)__ldg(vx + blk));
-  }
-#pragma unroll
-  for (int s = 16; s >= 1; s >>= 1) evmax = max(evmax, __shfl_xor_sync(0xffffffffu, evmax, s));
+    for (int s = 16; s >= 1; s >>= 1) evmax = max(evmax, __shfl_xor_sync(0xffffffffu, evmax, s));
 
-  float m[NT][2], l[NT][2], o[kN / 2][NT][4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) m[n][e] = -INFINITY, l[n][e] = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kN / 2; ++i)
+    float m[NT][2], l[NT][2], o[kN / 2][NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][n][e] = 0.0f;
-
-  int slot = 0;
-  uint32_t ph = 0;
-  bool late = false;
-  for (int q = warp; q < steps; q += kFewWarps) {
-    const int blk = kt.tile(i0 + (q >> 1)), j0 = blk * 64 + (q & 1) * kStep;
-    const int ke = (int)__ldg(kx + blk), ve = (int)__ldg(vx + blk);  // a tile starts below len
-    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[slot], ph, nullptr, kFewWaitNs))) {
-      if (lane == 0) set_error(p.hdr, SB_ETIMEOUT);
-      late = true;
-      break;
-    }
-    const uint32_t kbox = ring + (uint32_t)(slot * 2 * kBox), vbox = kbox + kBox;
-    float x[2][NT][4];  // tokens 16a + g (rows 2t, 2t + 1), 16a + g + 8
+      for (int e = 0; e < 2; ++e) m[n][e] = -INFINITY, l[n][e] = 0.0f;
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
+    for (int i = 0; i < kN / 2; ++i)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[a][n][e] = 0.0f;
-#pragma unroll
-      for (int c = 0; c < kC; ++c) {
-        const uint4 lo = ld_shared_v4(box_addr<D>(kbox, 16 * a + g, 64 * c + 16 * t));
-        const uint4 hi = ld_shared_v4(box_addr<D>(kbox, 16 * a + g + 8, 64 * c + 16 * t));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t k0 = i == 0 ? lo.x : i == 1 ? lo.y : i == 2 ? lo.z : lo.w;
-          const uint32_t k1 = i == 0 ? hi.x : i == 1 ? hi.y : i == 2 ? hi.z : hi.w;
-          const uint32_t a0 = e4m3x2_f16x2(k0), a1 = e4m3x2_f16x2(k1);
-          const uint32_t a2 = e4m3x2_f16x2(k0 >> 16), a3 = e4m3x2_f16x2(k1 >> 16);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma_16816(x[a][n], a0, a1, a2, a3, qf[n][c][i][0], qf[n][c][i][1]);
-        }
+        for (int e = 0; e < 4; ++e) o[i][n][e] = 0.0f;
+
+    for (int q = warp; q < steps; q += kFewWarps) {
+      const int blk = kt.tile(i0 + (q >> 1)), j0 = blk * 64 + (q & 1) * kStep;
+      const int ke = (int)__ldg(kx + blk), ve = (int)__ldg(vx + blk);  // a tile starts below len
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[slot], ph, nullptr, kFewWaitNs))) {
+        if (lane == 0) set_error(p.hdr, SB_ETIMEOUT);
+        late = true;
+        break;
       }
-    }
-    const int rel = max(ve - evmax, -64);
-    const float ev = (float)rel, iv = __uint_as_float((uint32_t)(127 - rel) << 23), ks = pow2_byte(ke);
-    const bool mask = tile_needs_mask(p, j0, kStep, pmin, pmax);
-    uint32_t w[2][NT][2];
+      const uint32_t kbox = ring + (uint32_t)(slot * 2 * kBox), vbox = kbox + kBox;
+      float x[2][NT][4];  // tokens 16a + g (rows 2t, 2t + 1), 16a + g + 8
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float f[2];
+      for (int a = 0; a < 2; ++a) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (mask) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int a = 0; a < 2; ++a)
+          for (int e = 0; e < 4; ++e) x[a][n][e] = 0.0f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (!key_visible(p, pos[n][e], j0 + 16 * a + 8 * h + g)) x[a][n][2 * h + e] = -INFINITY;
-        }
-        float mx = fmaxf(fmaxf(x[0][n][e], x[0][n][2 + e]), fmaxf(x[1][n][e], x[1][n][2 + e]));
+        for (int c = 0; c < kC; ++c) {
+          const uint4 lo = ld_shared_v4(box_addr<D>(kbox, 16 * a + g, 64 * c + 16 * t));
+          const uint4 hi = ld_shared_v4(box_addr<D>(kbox, 16 * a + g + 8, 64 * c + 16 * t));
 #pragma unroll
-        for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-        const float c = fminf(fmaxf(qc[n][e] * ks, 0x1p-126f), 0x1p126f);
-        const float mn = fmaxf(m[n][e], fmaf(mx, c, ev));
-        f[e] = 1.0f;
-        if (mn > m[n][e] + kRise) {
-          f[e] = fast_ex2(m[n][e] - mn);
-          m[n][e] = mn;
-          l[n][e] *= f[e];
-        }
-        const float add = ev - (m[n][e] == -INFINITY ? 0.0f : m[n][e]);
-        float sum = 0.0f;
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t k0 = i == 0 ? lo.x : i == 1 ? lo.y : i == 2 ? lo.z : lo.w;
+            const uint32_t k1 = i == 0 ? hi.x : i == 1 ? hi.y : i == 2 ? hi.z : hi.w;
+            const uint32_t a0 = e4m3x2_f16x2(k0), a1 = e4m3x2_f16x2(k1);
+            const uint32_t a2 = e4m3x2_f16x2(k0 >> 16), a3 = e4m3x2_f16x2(k1 >> 16);
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            x[a][n][2 * h + e] = fast_ex2(fmaf(x[a][n][2 * h + e], c, add));
-            sum += x[a][n][2 * h + e];
+            for (int n = 0; n < NT; ++n) mma_16816(x[a][n], a0, a1, a2, a3, qf[n][c][i][0], qf[n][c][i][1]);
           }
         }
-        l[n][e] = fmaf(sum, iv, l[n][e]);  // this lane's tokens
       }
-      if (__any_sync(0xffffffffu, f[0] != 1.0f || f[1] != 1.0f)) {
+      const int rel = max(min(ve - evmax, 0), -64);  // a tile past the end has any exponent
+      const float ev = (float)rel, iv = __uint_as_float((uint32_t)(127 - rel) << 23), ks = pow2_byte(ke);
+      const bool mask = tile_needs_mask(p, j0, kStep, pmin, pmax);
+      uint32_t w[2][NT][2];
 #pragma unroll
-        for (int i = 0; i < kN / 2; ++i) {
-          o[i][n][0] *= f[0], o[i][n][1] *= f[1];
-          o[i][n][2] *= f[0], o[i][n][3] *= f[1];
+      for (int n = 0; n < NT; ++n) {
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (mask) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (!key_visible(p, pos[n][e], j0 + 16 * a + 8 * h + g)) x[a][n][2 * h + e] = -INFINITY;
+          }
+          float mx = fmaxf(fmaxf(x[0][n][e], x[0][n][2 + e]), fmaxf(x[1][n][e], x[1][n][2 + e]));
+#pragma unroll
+          for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+          const float c = fminf(fmaxf(qc[n][e] * ks, 0x1p-126f), 0x1p126f);
+          const float mn = fmaxf(m[n][e], fmaf(mx, c, ev));
+          f[e] = 1.0f;
+          if (mn > m[n][e] + kRise) {
+            f[e] = fast_ex2(m[n][e] - mn);
+            m[n][e] = mn;
+            l[n][e] *= f[e];
+          }
+          const float add = ev - (m[n][e] == -INFINITY ? 0.0f : m[n][e]);
+          float sum = 0.0f;
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              x[a][n][2 * h + e] = fast_ex2(fmaf(x[a][n][2 * h + e], c, add));
+              sum += x[a][n][2 * h + e];
+            }
+          }
+          l[n][e] = fmaf(sum, iv, l[n][e]);  // this lane's tokens
+        }
+        if (__any_sync(0xffffffffu, f[0] != 1.0f || f[1] != 1.0f)) {
+#pragma unroll
+          for (int i = 0; i < kN / 2; ++i) {
+            o[i][n][0] *= f[0], o[i][n][1] *= f[1];
+            o[i][n][2] *= f[0], o[i][n][3] *= f[1];
+          }
+        }
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) w[a][n][h] = transpose8(pack_f16(x[a][n][2 * h], x[a][n][2 * h + 1]));
+      }
+      // zero what must not meet a weight of zero: codes past the end (they may be NaN), and blocks more
+      // than 2^64 below the largest
+      const int fine = ve < evmax - 64 ? 0 : sp.len - j0;
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        uint32_t e[4][kN / 4];  // tokens 16a + {2t, 2t+1, 2t+8, 2t+9}, channels kN g ..
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tok = 16 * a + 2 * t + (i & 1) + 8 * (i >> 1);
+          const uint32_t addr = box_addr<D>(vbox, tok, kN * g);
+          if constexpr (D == 128) {
+            const uint4 v = ld_shared_v4(addr);
+            e[i][0] = v.x, e[i][1] = v.y, e[i][2] = v.z, e[i][3] = v.w;
+          } else {
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(e[i][0]), "=r"(e[i][1]) : "r"(addr));
+          }
+          if (fine < kStep && tok >= fine) {
+#pragma unroll
+            for (int c = 0; c < kN / 4; ++c) e[i][c] = 0u;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < kN / 4; ++c) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // channels 4c + 2h (row g) and 4c + 2h + 1 (row g + 8)
+            const uint32_t lo = __byte_perm(e[0][c], e[1][c], h ? 0x7362 : 0x5140);
+            const uint32_t hi = __byte_perm(e[2][c], e[3][c], h ? 0x7362 : 0x5140);
+            const uint32_t a0 = e4m3x2_f16x2(lo), a1 = e4m3x2_f16x2(lo >> 16);
+            const uint32_t a2 = e4m3x2_f16x2(hi), a3 = e4m3x2_f16x2(hi >> 16);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_16816(o[2 * c + h][n], a0, a1, a2, a3, w[a][n][0], w[a][n][1]);
+          }
         }
       }
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) w[a][n][h] = transpose8(pack_f16(x[a][n][2 * h], x[a][n][2 * h + 1]));
+      __syncwarp();  // every lane has read the slot
+      if (lane == 0) fetch(slot, q + kFewSlots * kFewWarps);
+      if (++slot == kFewSlots) slot = 0, ph ^= 1u;
     }
-    // zero what must not meet a weight of zero: codes past the end (they may be NaN), and blocks more
-    // than 2^64 below the largest
-    const int fine = ve < evmax - 64 ? 0 : sp.len - j0;
-#pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      uint32_t e[4][kN / 4];  // tokens 16a + {2t, 2t+1, 2t+8, 2t+9}, channels kN g ..
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tok = 16 * a + 2 * t + (i & 1) + 8 * (i >> 1);
-        const uint32_t addr = box_addr<D>(vbox, tok, kN * g);
-        if constexpr (D == 128) {
-          const uint4 v = ld_shared_v4(addr);
-          e[i][0] = v.x, e[i][1] = v.y, e[i][2] = v.z, e[i][3] = v.w;
-        } else {
-          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(e[i][0]), "=r"(e[i][1]) : "r"(addr));
-        }
-        if (fine < kStep && tok >= fine) {
-#pragma unroll
-          for (int c = 0; c < kN / 4; ++c) e[i][c] = 0u;
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < kN / 4; ++c) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {  // channels 4c + 2h (row g) and 4c + 2h + 1 (row g + 8)
-          const uint32_t lo = __byte_perm(e[0][c], e[1][c], h ? 0x7362 : 0x5140);
-          const uint32_t hi = __byte_perm(e[2][c], e[3][c], h ? 0x7362 : 0x5140);
-          const uint32_t a0 = e4m3x2_f16x2(lo), a1 = e4m3x2_f16x2(lo >> 16);
-          const uint32_t a2 = e4m3x2_f16x2(hi), a3 = e4m3x2_f16x2(hi >> 16);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma_16816(o[2 * c + h][n], a0, a1, a2, a3, w[a][n][0], w[a][n][1]);
-        }
-      }
+    if (late) {  // what is still in flight lands before the memory is used again
+      for (int u = 0; u < kFewSlots; ++u, ph ^= slot == kFewSlots - 1, slot = slot + 1 == kFewSlots ? 0 : slot + 1)
+        mbar_wait_bounded(&full[slot], ph, nullptr, kFewDrainNs);
     }
-    __syncwarp();  // every lane has read the slot
-    if (lane == 0) fetch(slot, q + kFewSlots * kFewWarps);
-    if (++slot == kFewSlots) slot = 0, ph ^= 1u;
-  }
-  if (late) {  // what is still in flight lands before the memory is used again
-    for (int u = 0; u < kFewSlots; ++u, ph ^= slot == kFewSlots - 1, slot = slot + 1 == kFewSlots ? 0 : slot + 1)
-      mbar_wait_bounded(&full[slot], ph, nullptr, kFewDrainNs);
-  }
-  asm volatile("griddepcontrol.launch_dependents;");  // the join waits for this launch's end itself
+    // the last share: the joining launch may come up (it waits for this one's end itself)
+    if (deal && at + (i1 - i0) >= at_end) asm volatile("griddepcontrol.launch_dependents;");
 
-  // join the warps: sums over the lanes of a row, then warp after warp in shared memory
+    // join the warps: sums over the lanes of a row, then warp after warp in shared memory
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int s = 4; s < 32; s <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], s);
-  __syncthreads();  // the ring's memory is reused
-  constexpr int kRows = 8 * NT;
-  float* sm = reinterpret_cast<float*>(smem);  // [warp][row] m, then l, then [warp][row][D + 4] outputs
-  float* sl = sm + kFewWarps * kRows;
-  float* so = sl + kFewWarps * kRows;
+        for (int s = 4; s < 32; s <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], s);
+    __syncthreads();  // the ring's memory is reused
+    constexpr int kRows = 8 * NT;
+    float* sm = reinterpret_cast<float*>(smem);  // [warp][row] m, then l, then [warp][row][D + 4] outputs
+    float* sl = sm + kFewWarps * kRows;
+    float* so = sl + kFewWarps * kRows;
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = 8 * n + 2 * t + e;
-      if (g == 0) sm[warp * kRows + r] = m[n][e], sl[warp * kRows + r] = l[n][e];
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * n + 2 * t + e;
+        if (g == 0) sm[warp * kRows + r] = m[n][e], sl[warp * kRows + r] = l[n][e];
 #pragma unroll
-      for (int i = 0; i < kN / 2; ++i)
-        *reinterpret_cast<float2*>(&so[(warp * kRows + r) * (D + 4) + kN * g + 2 * i]) =
-            make_float2(o[i][n][e], o[i][n][2 + e]);
+        for (int i = 0; i < kN / 2; ++i)
+          *reinterpret_cast<float2*>(&so[(warp * kRows + r) * (D + 4) + kN * g + 2 * i]) =
+              make_float2(o[i][n][e], o[i][n][2 + e]);
+      }
     }
-  }
-  __syncthreads();
-  const float unit = __uint_as_float((uint32_t)max(evmax, 1) << 23);
-  for (int i = tid; i < rows * (D / 4); i += kFewThreads) {
-    const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
-    float mx = -INFINITY;
+    __syncthreads();
+    const float unit = __uint_as_float((uint32_t)max(evmax, 1) << 23);
+    for (int i = tid; i < rows * (D / 4); i += kFewThreads) {
+      const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
+      float mx = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kFewWarps; ++w) mx = fmaxf(mx, sm[w * kRows + r]);
-    float tot = 0.0f, y[4] = {};
+      for (int w = 0; w < kFewWarps; ++w) mx = fmaxf(mx, sm[w * kRows + r]);
+      float tot = 0.0f, y[4] = {};
 #pragma unroll
-    for (int w = 0; w < kFewWarps; ++w) {
-      const float mw = sm[w * kRows + r], f = mw == -INFINITY ? 0.0f : fast_ex2(mw - mx);
-      const float4 v = *reinterpret_cast<const float4*>(so + (w * kRows + r) * (D + 4) + c);
-      tot = fmaf(sl[w * kRows + r], f, tot);
-      y[0] = fmaf(v.x, f, y[0]), y[1] = fmaf(v.y, f, y[1]), y[2] = fmaf(v.z, f, y[2]), y[3] = fmaf(v.w, f, y[3]);
+      for (int w = 0; w < kFewWarps; ++w) {
+        const float mw = sm[w * kRows + r], f = mw == -INFINITY ? 0.0f : fast_ex2(mw - mx);
+        const float4 v = *reinterpret_cast<const float4*>(so + (w * kRows + r) * (D + 4) + c);
+        tot = fmaf(sl[w * kRows + r], f, tot);
+        y[0] = fmaf(v.x, f, y[0]), y[1] = fmaf(v.y, f, y[1]), y[2] = fmaf(v.z, f, y[2]), y[3] = fmaf(v.w, f, y[3]);
+      }
+      // nothing visible: zeros and -inf; a NaN row has a NaN sum and stays NaN
+      const float inv = tot > 0.0f ? unit / tot : tot;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] *= inv;
+      const float lse2 = tot > 0.0f ? mx + log2f(tot) : tot == 0.0f ? -INFINITY : tot;
+      const int tok = r / group;
+      const int64_t hq = hk * group + r - tok * group;
+      if (i1 - i0 == tiles) {  // the whole head
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + b * p.os[0] + tok * p.os[1] + hq * p.os[2] + c;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(__float_as_uint(y[0]), __float_as_uint(y[1])),
+                                                    pack_bf16x2(__float_as_uint(y[2]), __float_as_uint(y[3])));
+        if (p.lse && c == 0) p.lse[(b * p.heads_q + hq) * p.n_q + tok] = lse2 * 0.6931471805599453f;
+      } else {
+        const int side = i0 > 0 ? 0 : 1;  // taken over from the block before, or handed on
+        *reinterpret_cast<float4*>(few_part(part, D, blockIdx.x, side, r) + c) = make_float4(y[0], y[1], y[2], y[3]);
+        if (c == 0) *few_part_lse(part, D, gridDim.x, blockIdx.x, side, r) = lse2;
+      }
     }
-    // nothing visible: zeros and -inf; a NaN row has a NaN sum and stays NaN
-    const float inv = tot > 0.0f ? unit / tot : tot;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] *= inv;
-    const float lse2 = tot > 0.0f ? mx + log2f(tot) : tot == 0.0f ? -INFINITY : tot;
-    const int tok = r / group;
-    const int64_t hq = hk * group + r - tok * group;
-    if (splits == 1) {
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + b * p.os[0] + tok * p.os[1] + hq * p.os[2] + c;
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(__float_as_uint(y[0]), __float_as_uint(y[1])),
-                                                  pack_bf16x2(__float_as_uint(y[2]), __float_as_uint(y[3])));
-      if (p.lse && c == 0) p.lse[(b * p.heads_q + hq) * p.n_q + tok] = lse2 * 0.6931471805599453f;
-    } else {
-      *reinterpret_cast<float4*>(part_row(p, part, split, b, hk, r) + c) = make_float4(y[0], y[1], y[2], y[3]);
-      if (c == 0) *part_lse(p, part, splits, split, b, hk, r) = lse2;
-    }
+    at += i1 - i0;
+    if (!deal || at >= at_end) break;
+    fence_proxy_async_smem();  // the join's memory is the ring's again
+    if (__syncthreads_or(late)) break;
   }
 }
 
-// Joins the parts of a row: out = sum 2^(lse_s - max) o_s / sum 2^(lse_s - max). W warps per row, eight a
-// block: they take the parts in turn, a lane D / 32 channels, and meet in shared memory in a fixed order.
-// Parts that saw no key have lse -inf. Eight warps for many parts (a token), one for many rows.
-template <int D, int W>
-__global__ void __launch_bounds__(256) k_kv8_join(const Kv8Attn p, int splits, float* part) {
-  __shared__ float sy[8][D], st[8];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (p.prec && *p.prec == SB_SKIP) return;
-  constexpr int kE = D / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group = (int)(p.heads_q / p.c.heads);
-  const int64_t per = p.n_q * group;  // rows of a sequence and key head
-  const int64_t i = (int64_t)blockIdx.x * (8 / W) + warp / W;
-  if (i >= part_rows(p)) return;  // with W = 8 a block has one row
-  const int64_t bh = i / per, r = i - bh * per, b = bh / p.c.heads, hk = bh - b * p.c.heads;
-  const int64_t tok = r / group, hq = hk * group + r - tok * group;
-  if (tok >= sequence_span(p, b).nq) return;
-  float mx = -INFINITY;
-  for (int s = lane; s < splits; s += 32) mx = fmaxf(mx, __ldcg(part_lse(p, part, splits, s, b, hk, r)));
-  mx = warp_max_f32(mx);  // NaN parts are ignored here and make the sums NaN below
-  const float base = mx == -INFINITY ? 0.0f : mx;
-  float tot = 0.0f, y[kE] = {};
-#pragma unroll 4
-  for (int s = warp % W; s < splits; s += W) {
-    const float f = fast_ex2(__ldcg(part_lse(p, part, splits, s, b, hk, r)) - base);
-    const float* src = part_row(p, part, s, b, hk, r) + lane * kE;
-    tot += f;
-    if constexpr (D == 128) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-      y[0] = fmaf(v.x, f, y[0]), y[1] = fmaf(v.y, f, y[1]), y[2] = fmaf(v.z, f, y[2]), y[3] = fmaf(v.w, f, y[3]);
-    } else {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-      y[0] = fmaf(v.x, f, y[0]), y[1] = fmaf(v.y, f, y[1]);
-    }
-  }
-  if constexpr (W > 1) {
-#pragma unroll
-    for (int e = 0; e < kE; ++e) sy[warp][lane * kE + e] = y[e];
-    if (lane == 0) st[warp] = tot;
-    __syncthreads();
-    if (warp != 0) return;
-    tot = 0.0f;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) y[e] = 0.0f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      tot += st[w];
-#pragma unroll
-      for (int e = 0; e < kE; ++e) y[e] += sy[w][lane * kE + e];
-    }
-  }
+// One joined row: a lane writes its D / 32 channels.
+template <int D>
+__device__ __forceinline__ void put_joined(const Kv8Attn& p, int64_t b, int64_t hq, int64_t tok, int lane,
+                                           const float (&y)[D / 32], float tot, float mx) {
   const float inv = tot > 0.0f ? 1.0f / tot : tot;
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + b * p.os[0] + tok * p.os[1] +
-                                              hq * p.os[2] + lane * kE);
+                                              hq * p.os[2] + lane * (D / 32));
 #pragma unroll
-  for (int c = 0; c < kE / 2; ++c)
+  for (int c = 0; c < D / 64; ++c)
     dst[c] = pack_bf16x2(__float_as_uint(y[2 * c] * inv), __float_as_uint(y[2 * c + 1] * inv));
   if (p.lse && lane == 0)
     p.lse[(b * p.heads_q + hq) * p.n_q + tok] =
         tot > 0.0f ? (mx + log2f(tot)) * 0.6931471805599453f : tot == 0.0f ? -INFINITY : tot;
+}
+
+// Joins the parts of a dealt-out head: out = sum 2^(lse - max) o / sum 2^(lse - max). A block per row; its
+// warps take the parts in turn, a lane D / 32 channels, and meet in shared memory in a fixed order. Parts
+// that saw no key have lse -inf.
+template <int D>
+__global__ void __launch_bounds__(256) k_kv8_join_few(const Kv8Attn p, int blocks, float* part) {
+  __shared__ float sy[8][D], st[8];
+  constexpr int kE = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.prec && *p.prec == SB_SKIP) return;
+  const int group = (int)(p.heads_q / p.c.heads);
+  const int64_t per = p.n_q * group;  // rows of a sequence and key head
+  const int64_t bh = blockIdx.x / per, b = bh / p.c.heads, hk = bh - b * p.c.heads;
+  const int r = (int)(blockIdx.x - bh * per), tok = r / group;
+  const int64_t hq = hk * group + r - tok * group;
+  if (tok >= sequence_span(p, b).nq) return;
+  const FewPlace f = few_place(p, -1, (int)b, lane, false);
+  const int64_t shares = few_shares(f.total, blocks), t0 = f.before + hk * f.n;
+  const int64_t c0 = few_owner(t0, f.total, shares), c1 = few_owner(t0 + f.n - 1, f.total, shares);
+  if (c0 == c1) return;  // one block had the whole head
+  const int parts = (int)(c1 - c0) + 1;
+  float mx = -INFINITY;
+  for (int s = lane; s < parts; s += 32) mx = fmaxf(mx, __ldcg(few_part_lse(part, D, blocks, c0 + s, s == 0, r)));
+  mx = warp_max_f32(mx);  // NaN parts are ignored here and make the sums NaN below
+  const float base = mx == -INFINITY ? 0.0f : mx;
+  float tot = 0.0f, y[kE] = {};
+#pragma unroll 4
+  for (int s = warp; s < parts; s += 8) {
+    const float w = fast_ex2(__ldcg(few_part_lse(part, D, blocks, c0 + s, s == 0, r)) - base);
+    const float* src = few_part(part, D, c0 + s, s == 0, r) + lane * kE;
+    tot += w;
+    if constexpr (D == 128) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+      y[0] = fmaf(v.x, w, y[0]), y[1] = fmaf(v.y, w, y[1]), y[2] = fmaf(v.z, w, y[2]), y[3] = fmaf(v.w, w, y[3]);
+    } else {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+      y[0] = fmaf(v.x, w, y[0]), y[1] = fmaf(v.y, w, y[1]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < kE; ++e) sy[warp][lane * kE + e] = y[e];
+  if (lane == 0) st[warp] = tot;
+  __syncthreads();
+  if (warp != 0) return;
+  tot = 0.0f;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) y[e] = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    tot += st[w];
+#pragma unroll
+    for (int e = 0; e < kE; ++e) y[e] += sy[w][lane * kE + e];
+  }
+  put_joined<D>(p, b, hq, tok, lane, y, tot, mx);
+}
+
+// The same for the parts of the tensor-core kernel: many rows, few parts, a warp a row.
+template <int D>
+__global__ void __launch_bounds__(256) k_kv8_join(const Kv8Attn p, int splits, float* part) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.prec && *p.prec == SB_SKIP) return;
+  constexpr int kE = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int group = (int)(p.heads_q / p.c.heads);
+  const int64_t per = p.n_q * group;  // rows of a sequence and key head
+  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (i >= part_rows(p)) return;
+  const int64_t bh = i / per, r = i - bh * per, b = bh / p.c.heads, hk = bh - b * p.c.heads;
+  const int64_t tok = r / group, hq = hk * group + r - tok * group;
+  if (tok >= sequence_span(p, b).nq) return;
+  const float mine = lane < splits ? __ldcg(part_lse(p, part, splits, lane, b, hk, r)) : -INFINITY;
+  const float mx = warp_max_f32(mine);  // NaN parts are ignored here and make the sums NaN below
+  const float weight = fast_ex2(mine - (mx == -INFINITY ? 0.0f : mx));
+  float tot = 0.0f, y[kE] = {};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {  // at most 16
+    const float w = __shfl_sync(0xffffffffu, weight, s);
+    const float* src = part_row(p, part, s, b, hk, r) + lane * kE;
+    tot += w;
+    if constexpr (D == 128) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+      y[0] = fmaf(v.x, w, y[0]), y[1] = fmaf(v.y, w, y[1]), y[2] = fmaf(v.z, w, y[2]), y[3] = fmaf(v.w, w, y[3]);
+    } else {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+      y[0] = fmaf(v.x, w, y[0]), y[1] = fmaf(v.y, w, y[1]);
+    }
+  }
+  put_joined<D>(p, b, hq, tok, lane, y, tot, mx);
 }
 
 static bool cache_map(CUtensorMap* m, const uint8_t* base, const sb_kv8& c) {
@@ -438,7 +579,7 @@ static bool cache_map(CUtensorMap* m, const uint8_t* base, const sb_kv8& c) {
 }
 
 template <int D, int NT>
-static cudaError_t launch_few(const Kv8Attn& p, int splits, float* part, cudaStream_t s) {
+static cudaError_t launch_few(const Kv8Attn& p, int deal, unsigned grid, float* part, cudaStream_t s) {
   constexpr int kBytes = few_smem<D>() + 1024;  // + alignment of the dynamic base
   static_assert(kFewSlots * kFewWarps * 2 * kStep * D >= 4 * (kFewWarps * 16 * NT + kFewWarps * 8 * NT * (D + 4)),
                 "the join fits the ring");
@@ -447,31 +588,25 @@ static cudaError_t launch_few(const Kv8Attn& p, int splits, float* part, cudaStr
   if (e != cudaSuccess) return e;
   FewMaps tm;
   if (!cache_map(&tm.k, p.c.k_codes, p.c) || !cache_map(&tm.v, p.c.v_codes, p.c)) return cudaErrorInvalidValue;
-  k_kv8_few<D, NT><<<dim3((unsigned)splits, (unsigned)p.c.heads, (unsigned)p.c.batch), kFewThreads, kBytes, s>>>(
-      tm, p, splits, part);
+  k_kv8_few<D, NT><<<grid, kFewThreads, kBytes, s>>>(tm, p, deal, part);
   return cudaGetLastError();
 }
 
-// How the keys of a call are split. Few rows: one wave of the blocks that fit (two an SM with heads of
-// 128, four with 64), each with at least 256 tokens. Measured with parts for half a wave, one, one and a half,
-// two and four: 32 query and 8 key heads of 128, one sequence of 131071 tokens 62.8 / 52.6 / 62.2 / 56.6 /
-// 65.6 us, eight windows of 4099 tokens 23.5 / 19.4 / 25.1 / 22.1 / 27.5 us; 30 heads of 64, 17776 tokens 23.5 /
-// 21.4 / - / 27.0 us with a half, one and two waves. Many rows: the number of parts with the shortest
-// schedule of 148 CTAs, a part costing its key tiles and about three more for its start and its join.
+// Few rows: one wave of the blocks that fit (two an SM with heads of 128, four with 64); with many heads
+// (four waves of them) a block each, which is as even and needs no join.
+constexpr int64_t kFewUnits = 1184;
+static int few_blocks(int dim) { return dim == 64 ? 592 : 296; }
+
+// Many rows: the number of parts of the keys with the shortest schedule of 148 CTAs; a part costs its key
+// tiles and about six more (10 us) for its start and its end, and its results two passes over memory.
 static int plan_splits(int64_t batch, int64_t heads, int64_t heads_q, int64_t n_q, int dim, int64_t keys) {
-  const int64_t rows = n_q * (heads_q / heads), units = batch * heads;
+  const int64_t rows = n_q * (heads_q / heads), tiles = ceil_div(rows, 256) * batch * heads, len = ceil_div(keys, 128);
   const int64_t most = ((int64_t)128 << 20) / (batch * n_q * heads_q * dim * 4);  // 128 MB of partial results
-  if (rows <= kFewRows) {
-    const int64_t want = (dim == 64 ? 592 : 296) / units, fit = keys / 256;
-    int64_t s = want < fit ? want : fit;
-    s = s < most ? s : most;
-    return (int)(s > 1 ? s : 1);
-  }
-  const int64_t tiles = ceil_div(rows, 256) * units, len = ceil_div(keys, 128);
+  const int64_t join = batch * n_q * heads_q * dim * 4 / 400000;                  // of a part, in 1/16 key tiles (0.1 us)
   int best = 1;
-  int64_t cost = ceil_div(tiles, 148) * len * 16;
+  int64_t cost = ceil_div(tiles, 148) * (len * 16 + 96);
   for (int s = 2; s <= 16 && s <= most && s * 4 <= len; ++s) {
-    const int64_t c = ceil_div(tiles * s, 148) * (len * 16 / s + 48) + 48;
+    const int64_t c = ceil_div(tiles * s, 148) * (len * 16 / s + 96) + 40 + s * join;
     if (c < cost) cost = c, best = s;
   }
   return best;
@@ -483,41 +618,47 @@ cudaError_t launch_kv8_attention(const Kv8Attn& p, void* part_, cudaStream_t s, 
   using namespace kv8;
   *why = "sb_kv8_attention";
   float* part = static_cast<float*>(part_);
-  const int64_t rows = p.n_q * (p.heads_q / p.c.heads);
+  const int64_t rows = p.n_q * (p.heads_q / p.c.heads), units = p.c.batch * p.c.heads, all = part_rows(p);
+  if (rows <= kFewRows) {
+    const int deal = units < kFewUnits;
+    const unsigned grid = deal ? (unsigned)few_blocks(p.c.dim) : (unsigned)units;
+    cudaError_t e;
+    if (p.c.dim == 64)
+      e = rows <= 8 ? launch_few<64, 1>(p, deal, grid, part, s) : launch_few<64, 2>(p, deal, grid, part, s);
+    else
+      e = rows <= 8 ? launch_few<128, 1>(p, deal, grid, part, s) : launch_few<128, 2>(p, deal, grid, part, s);
+    if (e != cudaSuccess || !deal) return e;
+    *why = "sb_kv8_attention (join)";
+    const LaunchAfter L((unsigned)all, 256, 0, s, true);
+    return p.c.dim == 64 ? cudaLaunchKernelEx(&L.cfg, k_kv8_join_few<64>, p, (int)grid, part)
+                         : cudaLaunchKernelEx(&L.cfg, k_kv8_join_few<128>, p, (int)grid, part);
+  }
   int64_t keys = p.c.capacity;
   if (p.window > 0 && p.window + p.sinks + p.n_q < keys) keys = p.window + p.sinks + p.n_q;
   const int splits = plan_splits(p.c.batch, p.c.heads, p.heads_q, p.n_q, p.c.dim, keys);
-  cudaError_t e;
-  if (rows <= kFewRows) {
-    if (p.c.dim == 64)
-      e = rows <= 8 ? launch_few<64, 1>(p, splits, part, s) : launch_few<64, 2>(p, splits, part, s);
-    else
-      e = rows <= 8 ? launch_few<128, 1>(p, splits, part, s) : launch_few<128, 2>(p, splits, part, s);
-  } else {
-    e = launch_kv8_tiles(p, splits, part, s, why);
-  }
+  const cudaError_t e = launch_kv8_tiles(p, splits, part, s, why);
   if (e != cudaSuccess || splits == 1) return e;
   *why = "sb_kv8_attention (join)";
-  const int64_t all = part_rows(p);
-  const bool wide = splits > 16;
-  const LaunchAfter L((unsigned)(wide ? all : ceil_div(all, 8)), 256, 0, s, true);
-  if (p.c.dim == 64)
-    return wide ? cudaLaunchKernelEx(&L.cfg, k_kv8_join<64, 8>, p, splits, part)
-                : cudaLaunchKernelEx(&L.cfg, k_kv8_join<64, 1>, p, splits, part);
-  return wide ? cudaLaunchKernelEx(&L.cfg, k_kv8_join<128, 8>, p, splits, part)
-              : cudaLaunchKernelEx(&L.cfg, k_kv8_join<128, 1>, p, splits, part);
+  const LaunchAfter L((unsigned)ceil_div(all, 8), 256, 0, s, true);
+  return p.c.dim == 64 ? cudaLaunchKernelEx(&L.cfg, k_kv8_join<64>, p, splits, part)
+                       : cudaLaunchKernelEx(&L.cfg, k_kv8_join<128>, p, splits, part);
 }
 
 // The most that any number of key heads and any capacity need.
 size_t kv8_workspace_bytes(int64_t batch, int64_t heads_q, int64_t n_q, int dim) {
-  int64_t most = 0;
+  int64_t most = 0;  // floats
   for (int64_t heads = 1; heads <= heads_q; ++heads) {
     if (heads_q % heads) continue;
-    const int64_t s = kv8::plan_splits(batch, heads, heads_q, n_q, dim, (int64_t)1 << 30);
-    if (s > most) most = s;
+    int64_t f = 0;
+    if (n_q * (heads_q / heads) <= kv8::kFewRows) {
+      if (batch * heads < kv8::kFewUnits) f = (int64_t)kv8::few_blocks(dim) * 2 * kv8::kFewRows * (dim + 1);
+    } else {
+      const int64_t s = kv8::plan_splits(batch, heads, heads_q, n_q, dim, (int64_t)1 << 30);
+      if (s > 1) f = s * batch * n_q * heads_q * (dim + 1);
+    }
+    if (f > most) most = f;
   }
-  const int64_t rows = batch * n_q * heads_q;
-  return kKv8PartOffset + (most > 1 ? (size_t)(most * rows * (dim + 1) * 4 + 15) / 16 * 16 : 0);
+  return kKv8PartOffset + (size_t)(most * 4 + 15) / 16 * 16;
 }
 
 }  // namespace sb
