@@ -376,3 +376,29 @@ def test_offsets_past_32_bits(sbg, D, cap):
         assert (d <= 2.0 ** -7 * b.float().abs() + 2.0 ** -9).all() and first % 64 == 0
     del cache
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("B,H,Hq,D", [(33, 1, 1, 64), (70, 2, 4, 64), (70, 2, 2, 128), (300, 4, 4, 64), (1200, 1, 3, 64)])
+@pytest.mark.parametrize("n", [1, 3])
+def test_many_sequences_of_mixed_lengths(sbg, B, H, Hq, D, n):
+    """More sequences than a warp has lanes, among them empty ones and ones without queries; from 1184
+    heads on a block takes a whole head."""
+    g = torch.Generator().manual_seed(B)
+    lens = [int(x) for x in torch.randint(0, 300, (B,), generator=g)]
+    lens[0], lens[B // 2], lens[-1] = 0, 383, 1
+    p = Pair(sbg, B, H, 384, D)
+    p.fill(lens, seed=3)
+    attend(sbg, p, n, Hq, causal=True)
+    attend(sbg, p, n, Hq, nqs=[b % (n + 1) for b in range(B)], window=50, sinks=2)
+    attend(sbg, p, n, Hq, nqs=[0] * B)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,Hq,H", [(17, 1, 1), (40, 4, 2), (150, 2, 2)])
+def test_parts_of_long_caches(sbg, n, Hq, H, D):
+    """Few row tiles over long caches: the keys are split and the parts joined, some of them empty."""
+    p = Pair(sbg, 3, H, 8192, D)
+    p.fill([8100, 600, 3], seed=12)
+    attend(sbg, p, n, Hq, causal=True)
+    attend(sbg, p, n, Hq, nqs=[n, n - 5, 1])
+    attend(sbg, p, n, Hq, causal=True, window=900, sinks=130)

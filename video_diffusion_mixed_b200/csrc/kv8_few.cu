@@ -69,43 +69,6 @@ __device__ __forceinline__ int few_tiles(const Kv8Attn& p, const Span& sp) {
   return max(1, key_tiles(p, sp.pos(0), sp.pos(sp.nq - 1), 64).n);
 }
 
-// A place in the row of all tiles (sequence after sequence, key head after key head).
-struct FewPlace {
-  int64_t total;  // tiles of all
-  int64_t before; // tiles before sequence b
-  int b, n;       // the sequence, and the tiles of one of its key heads
-};
-// Whole warps: the place of tile t, or of sequence `seq` where seq >= 0. Reads every length (the host
-// takes this path for at most kFewUnits sequences).
-__device__ __forceinline__ FewPlace few_place(const Kv8Attn& p, int64_t t, int seq, int lane, bool report) {
-  FewPlace f{0, 0, -1, 0};
-  for (int64_t b0 = 0; b0 < p.c.batch; b0 += 32) {
-    const int64_t b = b0 + lane;
-    int n = 0;
-    if (b < p.c.batch) {
-      const Span sp = sequence_span(p, b);
-      if (report && sp.bad) set_error(p.hdr, SB_ESHAPE);
-      n = few_tiles(p, sp);
-    }
-    int64_t sum = n;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, sum, s);
-      if (lane >= s) sum += v;
-    }
-    const int64_t end = f.total + sum * p.c.heads, start = end - (int64_t)n * p.c.heads;
-    const bool here = seq >= 0 ? b == seq : n > 0 && t >= start && t < end;
-    const unsigned hit = __ballot_sync(0xffffffffu, here);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      f.b = (int)b0 + src;
-      f.n = __shfl_sync(0xffffffffu, n, src);
-      f.before = __shfl_sync(0xffffffffu, start, src);
-    }
-    f.total = __shfl_sync(0xffffffffu, end, 31);
-  }
-  return f;
-}
 // Blocks that get a share: at least four tiles each. Block c has the tiles [c total / shares, (c + 1) total /
 // shares); tile t belongs to the largest c with c total / shares <= t.
 __device__ __forceinline__ int64_t few_shares(int64_t total, int blocks) {
@@ -113,6 +76,76 @@ __device__ __forceinline__ int64_t few_shares(int64_t total, int blocks) {
 }
 __device__ __forceinline__ int64_t few_owner(int64_t t, int64_t total, int64_t shares) {
   return ((t + 1) * shares - 1) / total;
+}
+// A place in the row of all tiles (sequence after sequence, key head after key head).
+struct FewPlace {
+  int64_t total;  // tiles of all
+  int64_t before; // tiles before sequence b
+  int b, n;       // the sequence, and the tiles of one of its key heads
+};
+// Thirty-two sequences from b0 on, one a lane: its tiles, and the range of all its heads' tiles behind `base`.
+struct FewLane {
+  int n;
+  int64_t start, end;
+};
+__device__ __forceinline__ FewLane few_lane(const Kv8Attn& p, int64_t b0, int64_t base, int lane, bool report) {
+  FewLane f;
+  const int64_t b = b0 + lane;
+  f.n = 0;
+  if (b < p.c.batch) {
+    const Span sp = sequence_span(p, b);
+    if (report && sp.bad) set_error(p.hdr, SB_ESHAPE);
+    f.n = few_tiles(p, sp);
+  }
+  int64_t sum = f.n;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, sum, s);
+    if (lane >= s) sum += v;
+  }
+  f.end = base + sum * p.c.heads;
+  f.start = f.end - (int64_t)f.n * p.c.heads;
+  return f;
+}
+__device__ __forceinline__ void few_pick(const FewLane& l, int64_t b0, bool here, FewPlace& f) {
+  const unsigned hit = __ballot_sync(0xffffffffu, here);
+  if (hit) {
+    const int src = __ffs(hit) - 1;
+    f.b = (int)b0 + src;
+    f.n = __shfl_sync(0xffffffffu, l.n, src);
+    f.before = __shfl_sync(0xffffffffu, l.start, src);
+  }
+}
+// Whole warps: the place of tile t, or (seq >= 0) of a sequence. Reads every length: the host deals out
+// at most kFewUnits sequences.
+__device__ __forceinline__ FewPlace few_place(const Kv8Attn& p, int64_t t, int seq, int lane) {
+  FewPlace f{0, 0, -1, 0};
+  for (int64_t b0 = 0; b0 < p.c.batch; b0 += 32) {
+    const FewLane l = few_lane(p, b0, f.total, lane, false);
+    few_pick(l, b0, seq >= 0 ? b0 + lane == seq : t >= l.start && t < l.end, f);
+    f.total = __shfl_sync(0xffffffffu, l.end, 31);
+  }
+  return f;
+}
+// Block c of `blocks`: its share [at, at_end) of all tiles and the place of the first; false when it has none.
+__device__ __forceinline__ bool few_deal(const Kv8Attn& p, int c, int blocks, int lane, bool report, int64_t& at,
+                                         int64_t& at_end, FewPlace& f) {
+  FewLane l;
+  f = FewPlace{0, 0, -1, 0};
+  for (int64_t b0 = 0; b0 < p.c.batch; b0 += 32) {
+    l = few_lane(p, b0, f.total, lane, report);
+    f.total = __shfl_sync(0xffffffffu, l.end, 31);
+  }
+  const int64_t shares = few_shares(f.total, blocks);
+  if (c >= shares) return false;
+  at = c * f.total / shares;
+  at_end = (c + 1) * f.total / shares;
+  if (at >= at_end) return false;
+  if (p.c.batch <= 32)
+    few_pick(l, 0, at >= l.start && at < l.end, f);
+  else
+    f = few_place(p, at, -1, lane);
+  return true;
 }
 // Partial results: a block has at most two, of the head that it takes over and of the one it hands on.
 __device__ __forceinline__ float* few_part(float* part, int D, int64_t block, int side, int r) {
@@ -138,14 +171,8 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int group = (int)(p.heads_q / p.c.heads);
   int64_t at = 0, at_end = 0;
-  if (deal) {
-    const FewPlace f = few_place(p, -1, -1, lane, blockIdx.x == 0 && warp == 0);
-    const int64_t shares = few_shares(f.total, gridDim.x);
-    if (blockIdx.x >= shares) return;
-    at = blockIdx.x * f.total / shares;
-    at_end = (blockIdx.x + 1) * f.total / shares;
-    if (at >= at_end) return;
-  }
+  FewPlace place{0, 0, 0, 0};
+  if (deal && !few_deal(p, blockIdx.x, gridDim.x, lane, blockIdx.x == 0 && warp == 0, at, at_end, place)) return;
 
   // this warp's ring: slot s holds a box of keys, then one of values
   const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kFewSlots * 2 * kBox);
@@ -165,10 +192,10 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
     int64_t hk, b;
     int i0, i1, tiles;
     if (deal) {
-      const FewPlace f = few_place(p, at, -1, lane, false);
-      const int64_t in = at - f.before;
-      b = f.b;
-      tiles = f.n;
+      if (at >= place.before + place.n * p.c.heads) place = few_place(p, at, -1, lane);  // the next sequence
+      const int64_t in = at - place.before;
+      b = place.b;
+      tiles = place.n;
       hk = in / tiles;
       i0 = (int)(in - hk * tiles);
       i1 = (int)min((int64_t)tiles, i0 + (at_end - at));
@@ -493,7 +520,7 @@ __global__ void __launch_bounds__(256) k_kv8_join_few(const Kv8Attn p, int block
   const int r = (int)(blockIdx.x - bh * per), tok = r / group;
   const int64_t hq = hk * group + r - tok * group;
   if (tok >= sequence_span(p, b).nq) return;
-  const FewPlace f = few_place(p, -1, (int)b, lane, false);
+  const FewPlace f = few_place(p, -1, (int)b, lane);
   const int64_t shares = few_shares(f.total, blocks), t0 = f.before + hk * f.n;
   const int64_t c0 = few_owner(t0, f.total, shares), c1 = few_owner(t0 + f.n - 1, f.total, shares);
   if (c0 == c1) return;  // one block had the whole head

@@ -562,8 +562,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(stream):
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+# The current stream's handle, without the Stream object that torch.cuda.current_stream() builds (3 us a call).
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _raw_stream(stream, device: int):
+    return _current_raw_stream(device) if stream is None else stream.cuda_stream
 
 
 class Fp8Tensor:
@@ -625,7 +630,7 @@ def linear_fp8(X, a: Fp8Tensor, w: WeightFp8, Y, epilogue: int = EPI_NONE, prec=
     f32 = Y.dtype is torch.float32
     _typed(Y, torch.float32 if f32 else torch.bfloat16, (M, w.N), "Y")
     _ck(lib().sb_linear_fp8(_ptr(X), a._ref, _ptr(prec), w._ref, epilogue, OUT_F32 if f32 else OUT_BF16, Y.data_ptr(),
-                            M, ws.buf.data_ptr(), _raw_stream(stream)))
+                            M, ws.buf.data_ptr(), _raw_stream(stream, Y.get_device())))
 
 
 class KvCache8:
@@ -703,7 +708,8 @@ def kv8_store(k, v, cache: KvCache8, start=None, counts=None, prec=None, ws=None
     _typed(start, torch.int32, (cache.batch,), "start")
     _typed(counts, torch.int32, (cache.batch,), "counts")
     _ck(lib().sb_kv8_store(k.data_ptr(), _strides(k, "k"), v.data_ptr(), _strides(v, "v"), shape[1], cache._ref,
-                           _ptr(start), _ptr(counts), _ptr(prec), ws.buf.data_ptr(), _raw_stream(stream)))
+                           _ptr(start), _ptr(counts), _ptr(prec), ws.buf.data_ptr(),
+                           _raw_stream(stream, cache.device)))
 
 
 def kv8_attention(q, cache: KvCache8, out, lse=None, scale: float | None = None, causal: bool = False,
@@ -723,4 +729,4 @@ def kv8_attention(q, cache: KvCache8, out, lse=None, scale: float | None = None,
     opt = Attn(D ** -0.5 if scale is None else scale, bool(causal), window, sinks)
     _ck(lib().sb_kv8_attention(q.data_ptr(), _strides(q, "q"), n, Hq, cache._ref, ctypes.byref(opt), _ptr(q_lens),
                                out.data_ptr(), _strides(out, "out"), _ptr(lse), _ptr(prec), ws.buf.data_ptr(),
-                               ws.bytes, _raw_stream(stream)))
+                               ws.bytes, _raw_stream(stream, cache.device)))
