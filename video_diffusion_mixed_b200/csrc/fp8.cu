@@ -101,13 +101,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {  // 4, or 0: zero
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, int bytes) {  // 16, or 0: zero
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
 // 2^(a + b - 254) as two factors, so that no product in between leaves the range of FP32 when the
 // result does not.
 __device__ __forceinline__ float2 pow2_factors(uint32_t a, uint32_t b) {
@@ -122,25 +115,18 @@ __device__ __forceinline__ float2 pow2_factors(uint32_t a, uint32_t b) {
 //
 // A thread reads 16 consecutive channels of two weight rows and of one token: the order in which a
 // product's channels are summed is free, so the fragment's channels 2t, 2t+1, 2t+8, 2t+9 of step i are
-// channels 16t + 4i .. + 3 of both sides. All of it goes through shared memory only to be in flight
+// channels 16t + 4i .. + 3 of both sides. The weight's codes go through shared memory only to be in flight
 // without registers: each thread copies (cp.async) and reads back its own pieces, so no barrier is
-// needed. Two K-blocks deep, seven blocks fit an SM and 112 KB of weight are in flight. 1 x 11520 x 1920
-// with the weight out of L2's reach: 9.0 us (2.5 TB/s) with two slots, 9.7 with three, 11.3 with four
-// (fewer blocks an SM, and the reads of one do not hide the tail of another); 11.4 with the codes in
-// flight in registers.
+// needed, and four K-blocks a warp, all of a block's with K up to 2048, are on their way at once; the scales
+// and the tokens' codes follow in registers. 1 x 11520 x 1920 with the weight out of L2's reach: 8.2 us (2.7
+// TB/s; 6.7 us from L2), 1 x 7680 x 16384 30 us (4.2 TB/s). With the tokens' codes and the scales in the ring
+// too, which leaves room for two K-blocks in flight: 8.7 and 38 us; with all in registers 11.4.
 constexpr int kRowWarps = 4;
 constexpr int kRowThreads = kRowWarps * 32;
-constexpr int kRowSlots = 2;
-
-struct RowSlot {  // one K-block of every warp; [thread] is that thread's own
-  uint4 w[4][kRowThreads];         // piece 2c + r: chunk c (64 channels), weight row g + 8r
-  uint4 x[2][kRowThreads];         // chunk c of token g
-  uint32_t sw[2][kRowThreads];     // scale words of weight rows g, g + 8
-  uint32_t sx[2][kRowThreads];     // scale words of tokens 2t, 2t + 1
-};
+constexpr int kRowSlots = 4;
 
 __global__ void __launch_bounds__(kRowThreads) k_fp8_rows(Fp8Linear p) {
-  __shared__ RowSlot ring[kRowSlots];
+  __shared__ uint4 wbuf[kRowSlots][4][kRowThreads];  // piece 2c + r: chunk c (64 channels), weight row g + 8r
   __shared__ float red[kRowWarps][8][17];
   if (p.prec && *p.prec == SB_SKIP) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -152,73 +138,72 @@ __global__ void __launch_bounds__(kRowThreads) k_fp8_rows(Fp8Linear p) {
                         ((n0 & 127) >> 5);  // row n0 + g; row n0 + g + 8 is 32 words on
   const uint32_t* sfx = reinterpret_cast<const uint32_t*>(p.sfA);
   auto fetch_w = [&](int slot, int kb) {
-    if (kb >= nkb) return;
-    RowSlot& o = ring[slot];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int k = kb * 128 + c * 64;
       if (k < K) {
-        cp_async16(smem_u32(&o.w[2 * c][tid]), w0 + k);
-        cp_async16(smem_u32(&o.w[2 * c + 1][tid]), w1 + k);
+        cp_async16(smem_u32(&wbuf[slot][2 * c][tid]), w0 + k);
+        cp_async16(smem_u32(&wbuf[slot][2 * c + 1][tid]), w1 + k);
       }
     }
-    cp_async4(smem_u32(&o.sw[0][tid]), sfw + (int64_t)(kb >> 2) * 128, 4);
-    cp_async4(smem_u32(&o.sw[1][tid]), sfw + (int64_t)(kb >> 2) * 128 + 32, 4);
-  };
-  auto fetch_x = [&](int slot, int kb) {  // tokens past M read as zero
-    if (kb >= nkb) return;
-    RowSlot& o = ring[slot];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int k = kb * 128 + c * 64, e = 2 * t + c;
-      if (k < K)
-        cp_async16_or_zero(smem_u32(&o.x[c][tid]), p.A + (g < M ? (int64_t)g * K + k + 16 * t : 0), g < M ? 16 : 0);
-      cp_async4(smem_u32(&o.sx[c][tid]), sfx + (e < M ? (int64_t)(kb >> 2) * 128 + e * 4 : 0), e < M ? 4 : 0);
-    }
+    cp_async_commit();
   };
 #pragma unroll
-  for (int u = 0; u < kRowSlots; ++u) {
-    fetch_w(u, warp + u * kRowWarps);
-    cp_async_commit();
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the tokens' codes come from the launch before this one
-#pragma unroll
-  for (int u = 0; u < kRowSlots; ++u) {
-    fetch_x(u, warp + u * kRowWarps);
-    cp_async_commit();
-  }
+  for (int u = 0; u < kRowSlots; ++u) fetch_w(u, warp + u * kRowWarps);
   float total[4] = {};
-  int slot = 0;
-  for (int kb = warp; kb < nkb; kb += kRowWarps) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRowSlots - 1) : "memory");
-    const RowSlot& o = ring[slot];
-    float acc[4] = {};
+  bool waited = false;
+  for (int kb0 = warp; kb0 < nkb; kb0 += kRowSlots * kRowWarps) {
+    uint32_t sw[kRowSlots][2], sx[kRowSlots][2];
+    uint4 x[kRowSlots][2];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      if (kb * 128 + c * 64 >= K) break;
-      const uint4 wa = o.w[2 * c][tid], wb = o.w[2 * c + 1][tid], x = o.x[c][tid];
+    for (int u = 0; u < kRowSlots; ++u) {  // kb >> 2 is kb0 / 4 + u: a warp takes every fourth K-block
+      const int kb = kb0 + u * kRowWarps;
+      sw[u][0] = kb < nkb ? __ldg(sfw + (int64_t)(kb >> 2) * 128) : 0u;
+      sw[u][1] = kb < nkb ? __ldg(sfw + (int64_t)(kb >> 2) * 128 + 32) : 0u;
+    }
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the tokens' codes come from the launch before
+    waited = true;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t a = i == 0 ? wa.x : i == 1 ? wa.y : i == 2 ? wa.z : wa.w;
-        const uint32_t b = i == 0 ? wb.x : i == 1 ? wb.y : i == 2 ? wb.z : wb.w;
-        const uint32_t q = i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
-        mma_f16(acc, e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(b), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(b >> 16),
-                e4m3x2_to_f16x2(q), e4m3x2_to_f16x2(q >> 16));
+    for (int u = 0; u < kRowSlots; ++u) {  // tokens past M read as zero
+      const int kb = kb0 + u * kRowWarps;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int k = kb * 128 + c * 64, e = 2 * t + c;
+        x[u][c] = k < K && g < M ? ldg_v4(p.A + (int64_t)g * K + k + 16 * t) : make_uint4(0, 0, 0, 0);
+        sx[u][c] = kb < nkb && e < M ? __ldcg(sfx + (int64_t)(kb >> 2) * 128 + e * 4) : 0u;
       }
     }
-    const int sh = 8 * (kb & 3);
-    const uint32_t e0 = (o.sw[0][tid] >> sh) & 0xffu, e1 = (o.sw[1][tid] >> sh) & 0xffu;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t ex = (o.sx[j][tid] >> sh) & 0xffu;
-      const float2 f0 = pow2_factors(ex, e0), f1 = pow2_factors(ex, e1);
-      total[j] = fmaf(acc[j] * f0.x, f0.y, total[j]);
-      total[2 + j] = fmaf(acc[2 + j] * f1.x, f1.y, total[2 + j]);
+    for (int u = 0; u < kRowSlots; ++u) {
+      const int kb = kb0 + u * kRowWarps;
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRowSlots - 1) : "memory");
+      if (kb < nkb) {
+        float acc[4] = {};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (kb * 128 + c * 64 >= K) break;
+          const uint4 wa = wbuf[u][2 * c][tid], wb = wbuf[u][2 * c + 1][tid], q = x[u][c];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a = i == 0 ? wa.x : i == 1 ? wa.y : i == 2 ? wa.z : wa.w;
+            const uint32_t b = i == 0 ? wb.x : i == 1 ? wb.y : i == 2 ? wb.z : wb.w;
+            const uint32_t y = i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w;
+            mma_f16(acc, e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(b), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(b >> 16),
+                    e4m3x2_to_f16x2(y), e4m3x2_to_f16x2(y >> 16));
+          }
+        }
+        const int sh = 8 * (kb & 3);
+        const uint32_t e0 = (sw[u][0] >> sh) & 0xffu, e1 = (sw[u][1] >> sh) & 0xffu;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t ex = (sx[u][j] >> sh) & 0xffu;
+          const float2 f0 = pow2_factors(ex, e0), f1 = pow2_factors(ex, e1);
+          total[j] = fmaf(acc[j] * f0.x, f0.y, total[j]);
+          total[2 + j] = fmaf(acc[2 + j] * f1.x, f1.y, total[2 + j]);
+        }
+      }
+      fetch_w(u, kb + kRowSlots * kRowWarps);  // this thread has read its pieces of the slot
     }
-    fetch_w(slot, kb + kRowSlots * kRowWarps);  // this thread has read its pieces of the slot
-    fetch_x(slot, kb + kRowSlots * kRowWarps);
-    cp_async_commit();
-    slot = slot + 1 == kRowSlots ? 0 : slot + 1;
   }
   cp_async_wait_all();
 #pragma unroll
@@ -247,9 +232,9 @@ cudaError_t launch_fp8_linear(const Fp8Linear& p, cudaStream_t s, const char** w
     const cudaError_t e = launch_fp8_encode(p.X, p.M, p.K, p.prec, p.A, p.sfA, p.hdr, s);
     if (e != cudaSuccess) return e;
   }
-  // Up to one tile of tokens the stream wins: 4 x 1920 x 1920 4.6 us against 7.9 in the single form of
-  // the tensor-core product, 1 x 11520 x 1920 9.0 against 9.2, 8 x 7680 x 1920 8.6 against 9.1; two tiles
-  // lose (16 x 7680 x 1920: 11.0 against 8.3).
+  // Up to one tile of tokens the stream wins: 4 x 1920 x 1920 4.2 us against 7.9 in the single form of
+  // the tensor-core product, 1 x 11520 x 1920 8.2 against 9.2, 8 x 7680 x 1920 7.8 against 9.1; two tiles lost
+  // (16 x 7680 x 1920: 11.0 against 8.3).
   if (p.M > 8) return launch_fp8_gemm(p, s, why);
   *why = "sb_linear_fp8";
   const LaunchAfter L((unsigned)(p.N / 16), kRowThreads, 0, s, p.X != nullptr);
