@@ -402,3 +402,13 @@ def test_parts_of_long_caches(sbg, n, Hq, H, D):
     attend(sbg, p, n, Hq, causal=True)
     attend(sbg, p, n, Hq, nqs=[n, n - 5, 1])
     attend(sbg, p, n, Hq, causal=True, window=900, sinks=130)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("power", [-126, -118, -100, 100])
+def test_query_rows_at_the_ends_of_the_range(sbg, n, power):
+    """Rows near the smallest and the largest bf16 values, brought back by the scale: the power of two
+    that a row is multiplied with and the one that takes it back are the same."""
+    p = Pair(sbg, 1, 1, 256, 64)
+    p.fill([200], seed=9)
+    attend(sbg, p, n, 1, qscale=2.0 ** power, scale=0.125 * 2.0 ** -power)

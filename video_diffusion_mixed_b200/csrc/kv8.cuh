@@ -33,12 +33,13 @@ __device__ __forceinline__ float pow2_byte(int byte) {  // 2^(byte - 127)
 constexpr float kRise = 8.0f;  // log2 of how far a weight may pass 1 before the running maximum moves
 constexpr int kFewRows = 16;   // rows of a key head up to which the streaming kernel serves
 
-// The power of two that brings a row of queries with largest magnitude `a` (bf16 bits) to [2^14, 2^15),
-// and the factor of the scores that takes it and log2(e) back. An Inf or NaN stays one.
+// The power of two (at most 2^126) that brings a row of queries with largest magnitude `a` (bf16 bits) to
+// [2^14, 2^15), and the factor of the scores that takes it back, times scale and log2(e). An Inf or NaN
+// stays one.
 __device__ __forceinline__ float query_scale(float scale, uint32_t a, float& factor) {
-  const int e = min(141 - (int)(a >> 7), 127);  // 14 - floor(log2 a)
+  const int e = min(141 - (int)(a >> 7), 126);  // 14 - floor(log2 a)
   factor = __uint_as_float((uint32_t)(e + 127) << 23);
-  return scale * 1.4426950408889634f * __uint_as_float((uint32_t)max(127 - e, 1) << 23);
+  return scale * __uint_as_float((uint32_t)(127 - e) << 23) * 1.4426950408889634f;
 }
 
 // One sequence: tokens held, queries, and the position of a query token.

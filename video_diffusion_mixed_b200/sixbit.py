@@ -604,7 +604,7 @@ class WeightFp8:
         self._c = WeightFp8C()
         self._ref = ctypes.byref(self._c)
         self._c.w = self.w.c()
-        ws = ws or Workspace(1, 1, W.device, stream)
+        self._ws = ws = ws or Workspace(1, 1, W.device, stream)  # alive while the preparation runs
         _ck(lib().sb_prepare_weight_fp8(_ptr(W), _ptr(bias), N, K, ctypes.byref(self._c), ws.ptr, _stream(stream)))
 
     def c(self) -> WeightFp8C:
