@@ -502,7 +502,8 @@ typedef struct {
   uint8_t* k_exp;    /* [batch][heads][capacity / 64] E8M0 */
   uint8_t* v_exp;    /* [batch][heads][capacity / 64] E8M0 */
   int32_t* lens;     /* [batch] tokens held, in [0, capacity]; the caller may lower it to drop tokens */
-  int64_t batch, heads, capacity; /* capacity % 64 == 0, <= 2^30; batch, heads <= 16384, batch * heads <= 2^20 */
+  int64_t batch, heads, capacity; /* capacity % 64 == 0, <= 2^30; batch, heads <= 16384,
+                                   * batch * heads <= 2^20, batch * heads * capacity < 2^37 */
   int32_t dim;                    /* 64 or 128 */
 } sb_kv8;
 

@@ -76,7 +76,7 @@ def cache(sb, **kw):
 BAD_CACHES = [(dict(v_codes=None), "SB_EINVAL"), (dict(lens=None), "SB_EINVAL"), (dict(k_exp=0x3004), "SB_EALIGN"),
               (dict(dim=96), "SB_EUNSUPPORTED"), (dict(dim=0), "SB_EUNSUPPORTED"), (dict(batch=0), "SB_ESHAPE"),
               (dict(heads=20000), "SB_ESHAPE"), (dict(capacity=100), "SB_ESHAPE"), (dict(capacity=0), "SB_ESHAPE"),
-              (dict(batch=16384, heads=16384), "SB_ESHAPE")]
+              (dict(batch=16384, heads=16384), "SB_ESHAPE"), (dict(batch=256, heads=4, capacity=1 << 30), "SB_ESHAPE")]
 
 
 def test_store(sb):

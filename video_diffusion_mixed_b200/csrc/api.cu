@@ -997,6 +997,8 @@ static sb_status check_kv8(const sb_kv8* c) {
              SB_ESHAPE, "cache: batch and heads must be in [1, 16384], their product at most 2^20");
   SB_REQUIRE(c->capacity >= 64 && c->capacity <= (int64_t)1 << 30 && c->capacity % 64 == 0, SB_ESHAPE,
              "cache->capacity must be a multiple of 64 in [64, 2^30] (got %lld)", (long long)c->capacity);
+  SB_REQUIRE(c->capacity / 64 <= (((int64_t)1 << 31) - 1) / (c->batch * c->heads), SB_ESHAPE,
+             "cache: batch * heads * capacity must be below 2^37");
   return SB_OK;
 }
 

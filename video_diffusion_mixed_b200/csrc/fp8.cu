@@ -24,7 +24,10 @@ __device__ __forceinline__ uint32_t cvt_e4m3x4(float a, float b, float c, float 
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-// One warp per (row, 512 channels): a lane takes 16 channels, eight lanes a block.
+// One warp per (row, 512 channels): a lane takes 16 channels (two 16-byte loads, one 16-byte store of codes),
+// eight lanes a block, whose maximum takes three shuffles; four blocks make one 32-bit word of scales. Rows past
+// M up to the end of their atom get zero scales. Bound by memory (2 bytes read, 1 written an element):
+// 17776 x 1920 19.6 us (5.2 TB/s).
 __global__ void __launch_bounds__(256) k_fp8_encode(const __nv_bfloat16* __restrict__ X, int64_t M, int K,
                                                     const int32_t* prec, uint8_t* __restrict__ codes,
                                                     uint32_t* __restrict__ sf, WsHeader* hdr) {

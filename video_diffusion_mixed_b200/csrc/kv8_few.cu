@@ -16,6 +16,12 @@
 //      fragment to a right operand by 8 x 8 transposes in the register file.
 //
 // Block scales, the running maximum and its rare moves are those of the tensor-core kernel beside it.
+//
+// Measured (32 query heads, 8 key heads of 128, one token): 131071 tokens of one sequence 54 us (4.9 TB/s, the
+// join included), 32 sequences of 8191 tokens 95 us (5.7 TB/s), of 1 to 8191 tokens 75; 30 heads of 64, 17776
+// tokens 24 us. A block a head, with no join, takes 86 us for the 32 equal sequences but 84 for the mixed ones
+// (the longest block sets the time) and leaves most of the chip idle with few sequences. A long cache is
+// bound by the boxes in flight (DRAM at 64 percent) and by the start and the join, 8 us of the 54.
 #include <cudaTypedefs.h>
 
 #include "kv8.cuh"
@@ -69,58 +75,65 @@ __device__ __forceinline__ int few_tiles(const Kv8Attn& p, const Span& sp) {
   return max(1, key_tiles(p, sp.pos(0), sp.pos(sp.nq - 1), 64).n);
 }
 
-// Blocks that get a share: at least four tiles each. Block c has the tiles [c total / shares, (c + 1) total /
-// shares); tile t belongs to the largest c with c total / shares <= t.
-__device__ __forceinline__ int64_t few_shares(int64_t total, int blocks) {
-  return max((int64_t)1, min((int64_t)blocks, (total + 3) / 4));
-}
-__device__ __forceinline__ int64_t few_owner(int64_t t, int64_t total, int64_t shares) {
-  return ((t + 1) * shares - 1) / total;
-}
+// Blocks that get a share: one for every four tiles, as far as they go. The first `rem` of them have `base` + 1
+// tiles, the others `base`. All of this in 32 bits: a cache has fewer than 2^31 tiles.
+struct FewDeal {
+  int shares, base, rem;
+  __device__ __forceinline__ FewDeal(int total, int blocks) {
+    shares = max(1, min(blocks, (total - 1) / 4 + 1));
+    base = total / shares;
+    rem = total - base * shares;
+  }
+  __device__ __forceinline__ int first(int c) const { return c * base + min(c, rem); }
+  __device__ __forceinline__ int owner(int t) const {
+    const int wide = rem * (base + 1);
+    return t < wide ? t / (base + 1) : rem + (t - wide) / base;
+  }
+};
+
 // A place in the row of all tiles (sequence after sequence, key head after key head).
 struct FewPlace {
-  int64_t total;  // tiles of all
-  int64_t before; // tiles before sequence b
-  int b, n;       // the sequence, and the tiles of one of its key heads
+  int total;   // tiles of all
+  int before;  // tiles before sequence b
+  int b, n;    // the sequence, and the tiles of one of its key heads
 };
 // Thirty-two sequences from b0 on, one a lane: its tiles, and the range of all its heads' tiles behind `base`.
 struct FewLane {
-  int n;
-  int64_t start, end;
+  int n, start, end;
 };
-__device__ __forceinline__ FewLane few_lane(const Kv8Attn& p, int64_t b0, int64_t base, int lane, bool report) {
+__device__ __forceinline__ FewLane few_lane(const Kv8Attn& p, int b0, int base, int lane, bool report) {
   FewLane f;
-  const int64_t b = b0 + lane;
+  const int b = b0 + lane;
   f.n = 0;
   if (b < p.c.batch) {
     const Span sp = sequence_span(p, b);
     if (report && sp.bad) set_error(p.hdr, SB_ESHAPE);
     f.n = few_tiles(p, sp);
   }
-  int64_t sum = f.n;
+  int sum = f.n;
 #pragma unroll
   for (int s = 1; s < 32; s <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, sum, s);
+    const int v = __shfl_up_sync(0xffffffffu, sum, s);
     if (lane >= s) sum += v;
   }
-  f.end = base + sum * p.c.heads;
-  f.start = f.end - (int64_t)f.n * p.c.heads;
+  f.end = base + sum * (int)p.c.heads;
+  f.start = f.end - f.n * (int)p.c.heads;
   return f;
 }
-__device__ __forceinline__ void few_pick(const FewLane& l, int64_t b0, bool here, FewPlace& f) {
+__device__ __forceinline__ void few_pick(const FewLane& l, int b0, bool here, FewPlace& f) {
   const unsigned hit = __ballot_sync(0xffffffffu, here);
   if (hit) {
     const int src = __ffs(hit) - 1;
-    f.b = (int)b0 + src;
+    f.b = b0 + src;
     f.n = __shfl_sync(0xffffffffu, l.n, src);
     f.before = __shfl_sync(0xffffffffu, l.start, src);
   }
 }
 // Whole warps: the place of tile t, or (seq >= 0) of a sequence. Reads every length: the host deals out
 // at most kFewUnits sequences.
-__device__ __forceinline__ FewPlace few_place(const Kv8Attn& p, int64_t t, int seq, int lane) {
+__device__ __forceinline__ FewPlace few_place(const Kv8Attn& p, int t, int seq, int lane) {
   FewPlace f{0, 0, -1, 0};
-  for (int64_t b0 = 0; b0 < p.c.batch; b0 += 32) {
+  for (int b0 = 0; b0 < (int)p.c.batch; b0 += 32) {
     const FewLane l = few_lane(p, b0, f.total, lane, false);
     few_pick(l, b0, seq >= 0 ? b0 + lane == seq : t >= l.start && t < l.end, f);
     f.total = __shfl_sync(0xffffffffu, l.end, 31);
@@ -128,18 +141,18 @@ __device__ __forceinline__ FewPlace few_place(const Kv8Attn& p, int64_t t, int s
   return f;
 }
 // Block c of `blocks`: its share [at, at_end) of all tiles and the place of the first; false when it has none.
-__device__ __forceinline__ bool few_deal(const Kv8Attn& p, int c, int blocks, int lane, bool report, int64_t& at,
-                                         int64_t& at_end, FewPlace& f) {
+__device__ __forceinline__ bool few_deal(const Kv8Attn& p, int c, int blocks, int lane, bool report, int& at,
+                                         int& at_end, FewPlace& f) {
   FewLane l;
   f = FewPlace{0, 0, -1, 0};
-  for (int64_t b0 = 0; b0 < p.c.batch; b0 += 32) {
+  for (int b0 = 0; b0 < (int)p.c.batch; b0 += 32) {
     l = few_lane(p, b0, f.total, lane, report);
     f.total = __shfl_sync(0xffffffffu, l.end, 31);
   }
-  const int64_t shares = few_shares(f.total, blocks);
-  if (c >= shares) return false;
-  at = c * f.total / shares;
-  at_end = (c + 1) * f.total / shares;
+  const FewDeal d(f.total, blocks);
+  if (c >= d.shares) return false;
+  at = d.first(c);
+  at_end = d.first(c + 1);
   if (at >= at_end) return false;
   if (p.c.batch <= 32)
     few_pick(l, 0, at >= l.start && at < l.end, f);
@@ -170,7 +183,7 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
   if (p.prec && *p.prec == SB_SKIP) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int group = (int)(p.heads_q / p.c.heads);
-  int64_t at = 0, at_end = 0;
+  int at = 0, at_end = 0;
   FewPlace place{0, 0, 0, 0};
   if (deal && !few_deal(p, blockIdx.x, gridDim.x, lane, blockIdx.x == 0 && warp == 0, at, at_end, place)) return;
 
@@ -192,13 +205,13 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
     int64_t hk, b;
     int i0, i1, tiles;
     if (deal) {
-      if (at >= place.before + place.n * p.c.heads) place = few_place(p, at, -1, lane);  // the next sequence
-      const int64_t in = at - place.before;
+      if (at >= place.before + place.n * (int)p.c.heads) place = few_place(p, at, -1, lane);  // the next sequence
+      const int in = at - place.before, h = in / place.n;
       b = place.b;
+      hk = h;
       tiles = place.n;
-      hk = in / tiles;
-      i0 = (int)(in - hk * tiles);
-      i1 = (int)min((int64_t)tiles, i0 + (at_end - at));
+      i0 = in - h * tiles;
+      i1 = min(tiles, i0 + (at_end - at));
     } else {
       b = blockIdx.x / p.c.heads;
       hk = blockIdx.x - b * p.c.heads;
@@ -521,10 +534,10 @@ __global__ void __launch_bounds__(256) k_kv8_join_few(const Kv8Attn p, int block
   const int64_t hq = hk * group + r - tok * group;
   if (tok >= sequence_span(p, b).nq) return;
   const FewPlace f = few_place(p, -1, (int)b, lane);
-  const int64_t shares = few_shares(f.total, blocks), t0 = f.before + hk * f.n;
-  const int64_t c0 = few_owner(t0, f.total, shares), c1 = few_owner(t0 + f.n - 1, f.total, shares);
+  const FewDeal d(f.total, blocks);
+  const int t0 = f.before + (int)hk * f.n, c0 = d.owner(t0), c1 = d.owner(t0 + f.n - 1);
   if (c0 == c1) return;  // one block had the whole head
-  const int parts = (int)(c1 - c0) + 1;
+  const int parts = c1 - c0 + 1;
   float mx = -INFINITY;
   for (int s = lane; s < parts; s += 32) mx = fmaxf(mx, __ldcg(few_part_lse(part, D, blocks, c0 + s, s == 0, r)));
   mx = warp_max_f32(mx);  // NaN parts are ignored here and make the sums NaN below
@@ -620,12 +633,14 @@ static cudaError_t launch_few(const Kv8Attn& p, int deal, unsigned grid, float* 
 }
 
 // Few rows: one wave of the blocks that fit (two an SM with heads of 128, four with 64); with many heads
-// (four waves of them) a block each, which is as even and needs no join.
+// (four waves of them) a block each, which is as even and needs no join: 200 sequences of 4096 tokens with 8
+// key heads of 128 259 us (6.5 TB/s).
 constexpr int64_t kFewUnits = 1184;
 static int few_blocks(int dim) { return dim == 64 ? 592 : 296; }
 
 // Many rows: the number of parts of the keys with the shortest schedule of 148 CTAs; a part costs its key
-// tiles and about six more (10 us) for its start and its end, and its results two passes over memory.
+// tiles and about six more (10 us) for its start and its end, and its results two passes over memory. 1350
+// tokens of 30 heads of 64 that see 11026 keys: 1 / 2 / 3 / 4 / 6 / 8 parts took 332 / 289 / 281 / 284 / 312 / 338 us.
 static int plan_splits(int64_t batch, int64_t heads, int64_t heads_q, int64_t n_q, int dim, int64_t keys) {
   const int64_t rows = n_q * (heads_q / heads), tiles = ceil_div(rows, 256) * batch * heads, len = ceil_div(keys, 128);
   const int64_t most = ((int64_t)128 << 20) / (batch * n_q * heads_q * dim * 4);  // 128 MB of partial results
