@@ -532,8 +532,8 @@ typedef struct {
 } sb_attn;
 
 /* out = softmax(scale * q k^T) v over the tokens that the cache holds. q, out: bf16, strides as for
- * sb_kv8_store; rows of out must overlap neither one another nor q, the cache or lse; heads_q is a multiple of cache->heads, query head
- * h reads key head h / (heads_q / heads). q_lens (device int32 [batch], NULL: n_q): the sequence's
+ * sb_kv8_store; rows of out must overlap neither one another nor q, the cache or lse; heads_q is a
+ * multiple of cache->heads, query head h reads key head h / (heads_q / heads). q_lens (device int32 [batch], NULL: n_q): the sequence's
  * queries are its first q_lens[b] rows; the rows behind them are left as they are in out and lse.
  * A query at position p sees key j iff j < lens[b], j <= p and (window == 0 or p - j < window or
  * j < sinks). A query that sees no key gives zeros and lse -inf. lse (nullable): FP32
