@@ -540,8 +540,9 @@ typedef struct {
  * [batch][heads_q][n_q], the natural log of the sum of exp(scale * q . k). Keys and values enter the
  * products exactly (values of blocks whose scale is more than 2^64 below the largest scale seen by the same
  * part of the work count as zero), queries exactly unless a component is more than 2^31 below its row's
- * largest; softmax weights are rounded to fp16 for the second product, all sums are FP32. Inference only:
- * no gradient is computed.
+ * largest; softmax weights are rounded to fp16 for the second product, all sums are FP32. A NaN
+ * that was stored (sb_kv8_store reports it) stays in its head of its sequence, but may reach queries there
+ * that do not see it: a weight of zero times a NaN is one. Inference only: no gradient is computed.
  * lens or q_lens out of range are clamped and SB_ESHAPE is reported by sb_check. ws_bytes: size of ws
  * (SB_ESHAPE if too small). */
 sb_status sb_kv8_attention(const void* q, const int64_t* q_strides, int64_t n_q, int64_t heads_q,

@@ -412,3 +412,30 @@ def test_query_rows_at_the_ends_of_the_range(sbg, n, power):
     p = Pair(sbg, 1, 1, 256, 64)
     p.fill([200], seed=9)
     attend(sbg, p, n, 1, qscale=2.0 ** power, scale=0.125 * 2.0 ** -power)
+
+
+@pytest.mark.parametrize("n", [1, 40, 300])
+def test_nan_in_the_cache_stays_in_its_head(sbg, n):
+    """A stored NaN is reported; other heads and sequences, and tiles that no query sees, are not touched by it."""
+    k, v = heads(2, 400, 2, 64, 21), heads(2, 400, 2, 64, 22)
+    q = heads(2, n, 2, 64, 23)
+
+    def run(v, **kw):
+        p = Pair(sbg, 2, 2, 512, 64)
+        sbg.kv8_store(k, v, p.gpu, ws=p.ws)
+        out = torch.empty_like(q)
+        ws = sbg.AttnWorkspace(2, 2, n, 64)
+        sbg.kv8_attention(q, p.gpu, out, ws=ws, **kw)
+        sbg.check(ws)
+        return out, p.ws
+
+    bad = v.clone()
+    bad[1, 10, 0, 5] = float("nan")
+    clean, _ = run(v)
+    got, ws = run(bad)
+    with pytest.raises(sbg.SixbitError) as e:
+        sbg.check(ws)
+    assert e.value.status == sbg.SB_ENONFINITE
+    assert torch.equal(got[0], clean[0]) and torch.equal(got[1, :, 1], clean[1, :, 1])
+    assert torch.isnan(got[1, :, 0]).any(-1).all()
+    assert torch.equal(run(bad, window=200)[0], run(v, window=200)[0])  # the block of token 10 ends at 64
