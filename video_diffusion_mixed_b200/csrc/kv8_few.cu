@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
       }
     }
     __syncthreads();
-    const float unit = __uint_as_float((uint32_t)max(evmax, 1) << 23);
+    const float unit = pow2_byte(evmax);
     for (int i = tid; i < rows * (D / 4); i += kFewThreads) {
       const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
       float mx = -INFINITY;
@@ -478,9 +478,9 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
         y[0] = fmaf(v.x, f, y[0]), y[1] = fmaf(v.y, f, y[1]), y[2] = fmaf(v.z, f, y[2]), y[3] = fmaf(v.w, f, y[3]);
       }
       // nothing visible: zeros and -inf; a NaN row has a NaN sum and stays NaN
-      const float inv = tot > 0.0f ? unit / tot : tot;
+      const float inv = tot > 0.0f ? 1.0f / tot : tot;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] *= inv;
+      for (int e = 0; e < 4; ++e) y[e] = y[e] * inv * unit;  // in this order no factor leaves the normal range
       const float lse2 = tot > 0.0f ? mx + log2f(tot) : tot == 0.0f ? -INFINITY : tot;
       const int tok = r / group;
       const int64_t hq = hk * group + r - tok * group;

@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
       } else {
         tc_fence_after();
         // nothing visible: zeros and -inf; a NaN row has a NaN sum and stays NaN
-        const float inv = l > 0.0f ? __uint_as_float((uint32_t)max(sh.evmax, 1) << 23) / l : l;
+        const float inv = l > 0.0f ? 1.0f / l : l, unit = pow2_byte(sh.evmax);
         const float lse2 = l > 0.0f ? m + log2f(l) : l == 0.0f ? -INFINITY : l;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
@@ -342,7 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
             for (int i = 0; i < 32; ++i) o[i] = 0u;
           }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+          for (int i = 0; i < 32; ++i)  // in this order no factor leaves the normal range
+            o[i] = __float_as_uint(__uint_as_float(o[i]) * inv * unit);
           if (!live) continue;
           if (splits == 1) {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + b * p.os[0] + tok * p.os[1] +
