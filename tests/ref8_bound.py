@@ -5,7 +5,7 @@ import numpy as np
 from ref8 import TOKENS, value_of, visible
 
 
-def attention(cache, q, nqs, scale, causal=False, window=0, sinks=0, gain=36):
+def attention(cache, q, nqs, scale, causal=False, window=0, sinks=0, gain=32):
     """(out, lse, bound of out, bound of lse) of q [B][n][Hq][D] FP64 over a ref8.Cache. Rows that see nothing
     give 0 and -inf. The bounds are those of this arithmetic, per key j with weight p_j (sum 1):
 

@@ -55,3 +55,66 @@ def test_values_of_the_largest_scales(sbg, n, power):
     p = Pair(sbg, 1, 2, 512, 64)
     p.store(heads(1, 450, 2, 64, 1), heads(1, 450, 2, 64, 2, 2.0 ** power))
     attend(sbg, p, heads(1, n, 2, 64, 3))
+
+
+def stepped(p, scales, scores, seed, blank=()):
+    """Blocks of 64 tokens whose values have these scales (log2) and whose keys these scores (in nats, for a
+    query of 8 in channel 0 at D = 64); a block in `blank` holds zeros in channels 32 and up."""
+    m = len(scales) * 64
+    k, v = heads(1, m, 1, 64, seed).float() * 0.3, heads(1, m, 1, 64, seed + 1).float()
+    k[..., 0] = torch.tensor(scores, dtype=torch.float32, device="cuda").repeat_interleave(64)[None, :, None]
+    v *= torch.tensor(scales, dtype=torch.float64, device="cuda").exp2().repeat_interleave(64)[None, :, None, None].float()
+    for b in blank:
+        v[:, 64 * b:64 * b + 64, :, 32:] = 0
+    p.store(k.to(torch.bfloat16), v.to(torch.bfloat16))
+    return m
+
+
+@pytest.mark.parametrize("n", [1, 20, 200])
+def test_blocks_of_different_scale_each_by_its_weight(sbg, n):
+    """Values 2^20 larger in blocks that get no weight: the others keep their precision."""
+    p = Pair(sbg, 1, 1, 512, 64)
+    stepped(p, [0, -20, 10, 20, -20, 5, -3, 0], [0, 0, -60, -60, 0, -60, 0, 0], 3)
+    q = heads(1, n, 1, 64, 5)
+    q[..., 0] = 8.0
+    ref, tol = attend(sbg, p, q)
+    assert np.median(tol / np.abs(ref)) < 0.02
+
+
+@pytest.mark.parametrize("n", [1, 20, 200])
+def test_small_blocks_under_large_ones(sbg, n):
+    """Equal scores, a block 2^12 to 2^24 larger that holds zeros in half the channels: what the others keep there."""
+    for gap in (12, 20, 24):
+        p = Pair(sbg, 1, 1, 512, 64)
+        stepped(p, [0, gap, 0, 0], [0, 0, 0, 0], 17, blank=(1,))
+        q = heads(1, n, 1, 64, 5)
+        q[..., 0] = 8.0
+        ref, tol = attend(sbg, p, q)
+        assert gap == 24 or np.median(tol[..., 32:] / np.abs(ref[..., 32:])) < 0.1  # at 2^-24 a half step is 2^-8 a key
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("nats", [14, 18, 22])
+def test_one_key_far_above_a_long_cache(sbg, n, D, nats):
+    """A first key that takes nearly all the weight and holds zeros: the output is what the other 131070 add up to."""
+    held = 131071
+    p = Pair(sbg, 1, 1, held + 1, D)
+    k, v = heads(1, held, 1, D, 1, 0.05), torch.ones(1, held, 1, D, dtype=torch.bfloat16, device="cuda")
+    v[..., ::3] = 3.0
+    k[..., 0] = 0
+    k[:, 0, :, 0], v[:, 0] = nats, 0
+    p.store(k, v)
+    q = heads(1, n, 1, D, 5)
+    q[..., 0] = 8.0
+    ref, tol = attend(sbg, p, q, scale=0.125)
+    if nats <= 18:  # the bound itself says something: 19.3 nats, the most of these rows, are 2^-27.8, and 2^-32 of that is 0.06
+        assert (tol < 0.1 * np.abs(ref)).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,Hq,H", [(1, 2, 2), (3, 4, 1), (40, 1, 1)])
+def test_whole_long_cache(sbg, n, Hq, H, D):
+    p = Pair(sbg, 1, H, 131072, D)
+    p.fill([131071], seed=31)
+    attend(sbg, p, heads(1, n, Hq, D, 33))

@@ -30,7 +30,14 @@ __device__ __forceinline__ float pow2_byte(int byte) {  // 2^(byte - 127)
   return byte <= 0 ? 0x1p-127f : __uint_as_float((uint32_t)byte << 23);
 }
 
-constexpr float kRise = 8.0f;  // log2 of how far a weight may pass 1 before the running maximum moves
+// A softmax weight is rounded to fp16 times 2^kShift: relative to the running maximum it is 2^kRise at most
+// before the maximum moves, 2^(kRise + kShift) stays in fp16's range, and the smallest weights, of which a long
+// cache has many, are rounded at 2^-(25 + kShift) of the largest. A rise of 4 and a shift of 11 would keep
+// sixteen times smaller ones, but the maximum moves more often: 2047 causal rows of 16 heads of 128 took 202 us
+// instead of 189, 17776 x 17776 of 30 heads of 64 3.54 ms instead of 3.46.
+constexpr float kRise = 8.0f;
+constexpr int kShift = 7;
+constexpr float kUnshift = 1.0f / (1 << kShift);
 constexpr int kFewRows = 16;   // rows of a key head up to which the streaming kernel serves
 
 // The power of two (at most 2^126) that brings a row of queries with largest magnitude `a` (bf16 bits) to

@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
         }
       }
       const int rel = max(min(ve - evmax, 0), -64);  // a tile past the end has any exponent
-      const float ev = (float)rel, iv = __uint_as_float((uint32_t)(127 - rel) << 23), ks = pow2_byte(ke);
+      const float ev = (float)rel, iv = __uint_as_float((uint32_t)(127 - rel - kShift) << 23), ks = pow2_byte(ke);
       const bool mask = tile_needs_mask(p, j0, kStep, pmin, pmax);
       uint32_t w[2][NT][2];
 #pragma unroll
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
             m[n][e] = mn;
             l[n][e] *= f[e];
           }
-          const float add = ev - (m[n][e] == -INFINITY ? 0.0f : m[n][e]);
+          const float add = ev + (float)kShift - (m[n][e] == -INFINITY ? 0.0f : m[n][e]);
           float sum = 0.0f;
 #pragma unroll
           for (int a = 0; a < 2; ++a) {
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
         y[0] = fmaf(v.x, f, y[0]), y[1] = fmaf(v.y, f, y[1]), y[2] = fmaf(v.z, f, y[2]), y[3] = fmaf(v.w, f, y[3]);
       }
       // nothing visible: zeros and -inf; a NaN row has a NaN sum and stays NaN
-      const float inv = tot > 0.0f ? 1.0f / tot : tot;
+      const float inv = tot > 0.0f ? kUnshift / tot : tot;
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[e] = y[e] * inv * unit;  // in this order no factor leaves the normal range
       const float lse2 = tot > 0.0f ? mx + log2f(tot) : tot == 0.0f ? -INFINITY : tot;

@@ -14,8 +14,8 @@
 // of w, and with it the running maximum, which is that of what w V sums; the row sum takes it out again
 // by an exact factor. Blocks more than 2^64 below the largest count as zero in V. Queries are scaled by
 // a power of two to [2^14, 2^15) and rounded to fp16, exact for every component within 2^-31 of the row's
-// largest. The maximum moves only when it would rise by more than 2^8 (fp16 has the room), so the
-// accumulator is rescaled rarely.
+// largest. The maximum moves only when it would rise by more than 2^8, so the accumulator is
+// rescaled rarely; the rest of fp16's range, 2^7, is given to small weights.
 //
 // Warps: 0-3 and 4-7 softmax of the two row tiles, 8-11 codes -> fp16, 12 MMA issue. A key tile is taken in
 // two steps of 64 keys (a scale block each); the weights overwrite their scores. The shared memory that
@@ -49,7 +49,7 @@ constexpr int kRegsNeeded = (int)(kRegsSoft * 256 + kRegsConv * 128 + kRegsMma *
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kSlab = 16384;  // 128 rows x 64 fp16, 128B swizzle
 
-struct TileExp {  // a scale block: 2^ek, ev (relative) and 2^-ev
+struct TileExp {  // a scale block: 2^ek, ev (relative) and 2^-(ev + kShift)
   float k, v, iv, pad;
 };
 
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
             }
           }
         }
-        const float add = te.v - (m == -INFINITY ? 0.0f : m);
+        const float add = te.v + (float)kShift - (m == -INFINITY ? 0.0f : m);
         const uint64_t cc = pack2(c, c), aa = pack2(add, add);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
       } else {
         tc_fence_after();
         // nothing visible: zeros and -inf; a NaN row has a NaN sum and stays NaN
-        const float inv = l > 0.0f ? 1.0f / l : l, unit = pow2_byte(sh.evmax);
+        const float inv = l > 0.0f ? kUnshift / l : l, unit = pow2_byte(sh.evmax);
         const float lse2 = l > 0.0f ? m + log2f(l) : l == 0.0f ? -INFINITY : l;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
         const int rel = max((tid ? ve[1] : ve[0]) - evmax, -64);
         te.k = pow2_byte(tid ? ke[1] : ke[0]);
         te.v = (float)rel;
-        te.iv = __uint_as_float((uint32_t)(127 - rel) << 23);
+        te.iv = __uint_as_float((uint32_t)(127 - rel - kShift) << 23);
       }
       put(k_s + s * kOp, kreg);
       fence_proxy_async_smem();
