@@ -538,12 +538,12 @@ typedef struct {
  * A query at position p sees key j iff j < lens[b], j <= p and (window == 0 or p - j < window or
  * j < sinks). A query that sees no key gives zeros and lse -inf. lse (nullable): FP32
  * [batch][heads_q][n_q], the natural log of the sum of exp(scale * q . k). Keys and values enter the
- * products exactly (values of blocks whose scale is more than 2^64 below the largest scale seen by the same
- * part of the work count as zero), queries exactly unless a component is more than 2^31 below its row's
- * largest. For the second product a softmax weight is rounded to fp16 together with its block's scale of V:
- * with P the row's largest such product, by half a step (2^-11 of itself) down to 2^-21 P and by 2^-32 P below,
- * so that n keys of less weight are lost up to n 2^-32 P. The row's sum and lse count every weight in full; all
- * sums are FP32. A NaN
+ * products exactly, queries exactly unless a component is more than 2^31 below its row's largest. For the
+ * second product a softmax weight is rounded to fp16 together with its block's scale of V: with P the largest such
+ * product of the keys that the row sees, by half a step (2^-11 of itself) down to 2^-21 P and by 2^-32 P below, so
+ * that n keys of less weight are lost up to n 2^-32 P. The row's sum and lse count every weight in full; all sums
+ * are FP32. Scales of any spread are sound; a head whose values differ by more than 2^64 from block to block may
+ * take some hundred times longer where there are more than 16 query rows for a key head. A NaN
  * that was stored (sb_kv8_store reports it) stays in its head of its sequence, but may reach queries there
  * that do not see it: a weight of zero times a NaN is one. Inference only: no gradient is computed.
  * lens or q_lens out of range are clamped and SB_ESHAPE is reported by sb_check. ws_bytes: size of ws

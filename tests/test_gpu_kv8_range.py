@@ -81,6 +81,26 @@ def test_blocks_of_different_scale_each_by_its_weight(sbg, n):
     assert np.median(tol / np.abs(ref)) < 0.02
 
 
+WIDE = {"small above large": ([60, -60], [0, 110]), "large above small": ([-60, 60], [110, 0]),
+        "far apart, equal": ([-100, 20, -100], [0, 0, 0]), "falling": ([100, 50, 0, -50, -100], [0, 50, 100, 150, 200]),
+        "rising": ([-100, -50, 0, 50, 100], [200, 150, 100, 50, 0]), "alternating": ([90, -90] * 4, [-150, 10] * 4),
+        "sum of the small": ([0, -120, 0, -120], [0, 80, 1, 81]), "ends": ([117, -126], [-180, 3])}
+
+
+@pytest.mark.parametrize("n", [1, 20, 200])
+@pytest.mark.parametrize("case", list(WIDE))
+def test_scales_further_apart_than_the_sums_range(sbg, n, case):
+    """Blocks whose scales differ by up to 2^243, scores that undo it: the sum and the output each keep
+    their precision."""
+    scales, scores = WIDE[case]
+    p = Pair(sbg, 1, 1, 512, 64)
+    stepped(p, scales, scores, 11)
+    q = heads(1, n, 1, 64, 5)
+    q[..., 0] = 8.0
+    attend(sbg, p, q)
+    attend(sbg, p, q, causal=True)
+
+
 @pytest.mark.parametrize("n", [1, 20, 200])
 def test_small_blocks_under_large_ones(sbg, n):
     """Equal scores, a block 2^12 to 2^24 larger that holds zeros in half the channels: what the others keep there."""
@@ -118,3 +138,26 @@ def test_whole_long_cache(sbg, n, Hq, H, D):
     p = Pair(sbg, 1, H, 131072, D)
     p.fill([131071], seed=31)
     attend(sbg, p, heads(1, n, Hq, D, 33))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,held,first", [(5, 130, 128), (16, 200, 192), (300, 448, 256), (384, 448, 320)])
+@pytest.mark.parametrize("power", [40, 70, 110])
+def test_later_tokens_leave_earlier_rows_alone(sbg, n, held, first, D, power):
+    """Causal: values of any size behind a query's position change nothing for it."""
+    p = Pair(sbg, 1, 2, 512, D)
+    k, v = heads(1, held, 2, D, 1), heads(1, held, 2, D, 2).float()
+    v[:, first:] *= 2.0 ** power
+    p.store(k, v.to(torch.bfloat16))
+    attend(sbg, p, heads(1, n, 2, D, 3), causal=True)
+
+
+@pytest.mark.parametrize("n", [5, 16, 300])
+def test_tokens_behind_the_window_leave_later_rows_alone(sbg, n):
+    p = Pair(sbg, 1, 2, 512, 64)
+    k, v = heads(1, 500, 2, 64, 1), heads(1, 500, 2, 64, 2).float()
+    v[:, :448] *= torch.tensor([2.0 ** 90, 1.0, 2.0 ** -80, 2.0 ** 70, 1.0, 2.0 ** 100, 1.0],
+                               device="cuda").repeat_interleave(64)[None, :, None, None]
+    p.store(k, v.to(torch.bfloat16))
+    for window, sinks in ((1, 0), (40, 0), (100, 3), (200, 70)):
+        attend(sbg, p, heads(1, n, 2, 64, 3), causal=True, window=window, sinks=sinks)

@@ -47,11 +47,6 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float fast_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {  // 8 x 8 matrix of 16-bit values
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
@@ -289,21 +284,13 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
         }
       }
     }
-    // the largest exponent of V over the block's share (while the first boxes are on their way)
-    const int blocks = (sp.len + 63) >> 6;
-    int evmax = 0;
-    for (int i = lane; i < i1 - i0; i += 32) {
-      const int blk = kt.tile(i0 + i);
-      if (blk < blocks) evmax = max(evmax, (int)__ldg(vx + blk));
-    }
-#pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) evmax = max(evmax, __shfl_xor_sync(0xffffffffu, evmax, s));
-
-    float m[NT][2], l[NT][2], o[kN / 2][NT][4];
+    const int e0 = (int)__ldg(vx + kt.tile(i0));  // exponents of V are taken relative to the share's first
+    float o[kN / 2][NT][4];
+    RowStats st[NT][2];  // l: this lane's tokens
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) m[n][e] = -INFINITY, l[n][e] = 0.0f;
+      for (int e = 0; e < 2; ++e) st[n][e] = RowStats{-INFINITY, 0.0f, 0};
 #pragma unroll
     for (int i = 0; i < kN / 2; ++i)
 #pragma unroll
@@ -342,8 +329,8 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
           }
         }
       }
-      const int rel = max(min(ve - evmax, 0), -64);  // a tile past the end has any exponent
-      const float ev = (float)rel, iv = __uint_as_float((uint32_t)(127 - rel - kShift) << 23), ks = pow2_byte(ke);
+      const int rel = ve - e0;
+      const float ev = (float)rel, ks = pow2_byte(ke);
       const bool mask = tile_needs_mask(p, j0, kStep, pmin, pmax);
       uint32_t w[2][NT][2];
 #pragma unroll
@@ -362,15 +349,23 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
 #pragma unroll
           for (int s = 4; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
           const float c = fminf(fmaxf(qc[n][e] * ks, 0x1p-126f), 0x1p126f);
-          const float mn = fmaxf(m[n][e], fmaf(mx, c, ev));
+          RowStats& r = st[n][e];
+          const float mn = fmaxf(r.m, fmaf(mx, c, ev));
           f[e] = 1.0f;
-          if (mn > m[n][e] + kRise) {
-            f[e] = fast_ex2(m[n][e] - mn);
-            m[n][e] = mn;
-            l[n][e] *= f[e];
+          if (mn > r.m + kRise) {
+            f[e] = fast_ex2(r.m - mn);
+            move_max(r, mn, rel);
           }
-          const float add = ev + (float)kShift - (m[n][e] == -INFINITY ? 0.0f : m[n][e]);
+          const int below = r.e - rel;
           float sum = 0.0f;
+          if (below > kFar) {
+            const float base = far_base(r, mx, c);
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) r.l += fast_ex2(fmaf(x[a][n][2 * h + e], c, base));
+          }
+          const float add = ev + (float)kShift - (r.m == -INFINITY ? 0.0f : r.m);
 #pragma unroll
           for (int a = 0; a < 2; ++a) {
 #pragma unroll
@@ -379,7 +374,7 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
               sum += x[a][n][2 * h + e];
             }
           }
-          l[n][e] = fmaf(sum, iv, l[n][e]);  // this lane's tokens
+          if (below <= kFar) r.l = fmaf(sum, sum_factor(below), r.l);
         }
         if (__any_sync(0xffffffffu, f[0] != 1.0f || f[1] != 1.0f)) {
 #pragma unroll
@@ -393,9 +388,7 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
 #pragma unroll
           for (int h = 0; h < 2; ++h) w[a][n][h] = transpose8(pack_f16(x[a][n][2 * h], x[a][n][2 * h + 1]));
       }
-      // zero what must not meet a weight of zero: codes past the end (they may be NaN), and blocks more
-      // than 2^64 below the largest
-      const int fine = ve < evmax - 64 ? 0 : sp.len - j0;
+      const int fine = sp.len - j0;  // codes past the end are zeroed: they may be NaN, which no weight of zero hides
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
         uint32_t e[4][kN / 4];  // tokens 16a + {2t, 2t+1, 2t+8, 2t+9}, channels kN g ..
@@ -444,18 +437,17 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int s = 4; s < 32; s <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], s);
+        for (int s = 4; s < 32; s <<= 1) st[n][e].l += __shfl_xor_sync(0xffffffffu, st[n][e].l, s);
     __syncthreads();  // the ring's memory is reused
     constexpr int kRows = 8 * NT;
-    float* sm = reinterpret_cast<float*>(smem);  // [warp][row] m, then l, then [warp][row][D + 4] outputs
-    float* sl = sm + kFewWarps * kRows;
-    float* so = sl + kFewWarps * kRows;
+    float* so = reinterpret_cast<float*>(smem);  // [warp][row][D + 4] outputs, then [warp][row] statistics
+    RowStats* ss = reinterpret_cast<RowStats*>(so + kFewWarps * kRows * (D + 4));
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = 8 * n + 2 * t + e;
-        if (g == 0) sm[warp * kRows + r] = m[n][e], sl[warp * kRows + r] = l[n][e];
+        if (g == 0) ss[warp * kRows + r] = st[n][e];
 #pragma unroll
         for (int i = 0; i < kN / 2; ++i)
           *reinterpret_cast<float2*>(&so[(warp * kRows + r) * (D + 4) + kN * g + 2 * i]) =
@@ -463,25 +455,38 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
       }
     }
     __syncthreads();
-    const float unit = pow2_byte(evmax);
     for (int i = tid; i < rows * (D / 4); i += kFewThreads) {
       const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
-      float mx = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) mx = fmaxf(mx, sm[w * kRows + r]);
-      float tot = 0.0f, y[4] = {};
+      RowStats all{-INFINITY, 0.0f, 0};
 #pragma unroll
       for (int w = 0; w < kFewWarps; ++w) {
-        const float mw = sm[w * kRows + r], f = mw == -INFINITY ? 0.0f : fast_ex2(mw - mx);
+        const RowStats one = ss[w * kRows + r];
+        if (one.m > all.m) all.m = one.m, all.e = one.e;
+      }
+      int down = 0;  // the joint sum's exponent gives way to the warp whose sum counts most
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) {
+        const RowStats one = ss[w * kRows + r];
+        const float y = one.m - all.m + (float)(all.e - one.e);
+        if (one.m != -INFINITY && y > 0.0f) down = max(down, min(__float2int_ru(y), 512));
+      }
+      all.e -= down;
+      float y[4] = {};
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) {
+        const RowStats one = ss[w * kRows + r];
+        const bool none = one.m == -INFINITY;  // a sum of zero, or NaN
+        const float f = none ? 0.0f : fast_ex2(one.m - all.m);
         const float4 v = *reinterpret_cast<const float4*>(so + (w * kRows + r) * (D + 4) + c);
-        tot = fmaf(sl[w * kRows + r], f, tot);
+        all.l = fmaf(one.l, none ? 0.0f : fast_ex2(one.m - all.m + (float)(all.e - one.e)), all.l);
         y[0] = fmaf(v.x, f, y[0]), y[1] = fmaf(v.y, f, y[1]), y[2] = fmaf(v.z, f, y[2]), y[3] = fmaf(v.w, f, y[3]);
       }
       // nothing visible: zeros and -inf; a NaN row has a NaN sum and stays NaN
-      const float inv = tot > 0.0f ? kUnshift / tot : tot;
+      const float inv = all.l > 0.0f ? 1.0f / all.l : all.l;
+      const float2 unit = output_unit(all.e, e0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = y[e] * inv * unit;  // in this order no factor leaves the normal range
-      const float lse2 = tot > 0.0f ? mx + log2f(tot) : tot == 0.0f ? -INFINITY : tot;
+      for (int e = 0; e < 4; ++e) y[e] = y[e] * unit.x * inv * unit.y;
+      const float lse2 = all.l > 0.0f ? all.m - (float)all.e + log2f(all.l) : all.l == 0.0f ? -INFINITY : all.l;
       const int tok = r / group;
       const int64_t hq = hk * group + r - tok * group;
       if (i1 - i0 == tiles) {  // the whole head
@@ -621,7 +626,7 @@ static bool cache_map(CUtensorMap* m, const uint8_t* base, const sb_kv8& c) {
 template <int D, int NT>
 static cudaError_t launch_few(const Kv8Attn& p, int deal, unsigned grid, float* part, cudaStream_t s) {
   constexpr int kBytes = few_smem<D>() + 1024;  // + alignment of the dynamic base
-  static_assert(kFewSlots * kFewWarps * 2 * kStep * D >= 4 * (kFewWarps * 16 * NT + kFewWarps * 8 * NT * (D + 4)),
+  static_assert(kFewSlots * kFewWarps * 2 * kStep * D >= kFewWarps * 8 * NT * ((int)sizeof(RowStats) + 4 * (D + 4)),
                 "the join fits the ring");
   static std::atomic<uint64_t> attr{0};
   const cudaError_t e = smem_attr_once(k_kv8_few<D, NT>, kBytes, attr);

@@ -10,12 +10,14 @@
 //
 // Keys and values are E4M3 codes, which fp16 holds exactly, so a warpgroup turns each tile's codes into
 // fp16 operands once for the 256 rows. The block scales are powers of two and never touch the tiles:
-// the keys' enters c, the values' exponent ev (relative to the largest of the CTA's range) the exponent
-// of w, and with it the running maximum, which is that of what w V sums; the row sum takes it out again
-// by an exact factor. Blocks more than 2^64 below the largest count as zero in V. Queries are scaled by
-// a power of two to [2^14, 2^15) and rounded to fp16, exact for every component within 2^-31 of the row's
-// largest. The maximum moves only when it would rise by more than 2^8, so the accumulator is
-// rescaled rarely; the rest of fp16's range, 2^7, is given to small weights.
+// the keys' enters c, the values' exponent ev the exponent of w, and with it the running maximum, which is
+// that of what w V sums; the row sum takes it out again by an exact factor (RowStats in kv8.cuh). A block of
+// values 2^64 below the largest before it is left out of the product, and if it holds anything but zeros the
+// CTA computes its rows again one by one in FP32: a branch for that in the softmax's loop, taken or not, cost a
+// tenth of the time of 17776 x 17776, a second loop behind it as much. Queries are scaled by a power of two to
+// [2^14, 2^15) and rounded to fp16, exact for every component within 2^-31 of the row's largest. The maximum
+// moves only when it would rise by more than 2^8, so the accumulator is rescaled rarely; the rest of fp16's
+// range, 2^7, is given to small weights.
 //
 // Warps: 0-3 and 4-7 softmax of the two row tiles, 8-11 codes -> fp16, 12 MMA issue. A key tile is taken in
 // two steps of 64 keys (a scale block each); the weights overwrite their scores. The shared memory that
@@ -49,8 +51,9 @@ constexpr int kRegsNeeded = (int)(kRegsSoft * 256 + kRegsConv * 128 + kRegsMma *
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kSlab = 16384;  // 128 rows x 64 fp16, 128B swizzle
 
-struct TileExp {  // a scale block: 2^ek, ev (relative) and 2^-(ev + kShift)
-  float k, v, iv, pad;
+struct TileExp {  // a scale block: 2^ek, and ev relative to the first block's
+  float k, v;
+  int e, pad;
 };
 
 struct TileShared {
@@ -62,8 +65,10 @@ struct TileShared {
 
   uint32_t tmem;
   int abort;
-  int evmax;  // largest exponent byte of V in the CTA's range
+  int e0;    // the exponent byte of V's first block
+  int redo;  // the rows are computed again, one by one
   TileExp exps[4][2];
+  float q[8][128];  // a softmax warp's row
 };
 
 template <int D>
@@ -137,19 +142,62 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // A row of a 128-row operand tile: 8 channels (16 bytes) at chunk c.
 __device__ __forceinline__ uint32_t tile_addr(uint32_t base, int row, int c) {
   return base + (uint32_t)((c >> 3) * kSlab + row * 128 + (((c & 7) ^ (row & 7)) << 4));
 }
 
+// The accumulator of row tile t is complete up to step u - 1 once that step's product is done; the phase before
+// is behind the scores just read, so the parity is not ambiguous.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int splits, float* part) {
+__device__ __forceinline__ bool rescale(TileShared& sh, int t, int u, uint32_t o_col, float f) {
+  if (!__all_sync(0xffffffffu, mbar_wait_bounded(&sh.o_done[t], (uint32_t)((u - 1) & 1), &sh.abort, kWaitNs))) return false;
+  tc_fence_after();
+#pragma unroll 1
+  for (int h = 0; h < D / 16; ++h) {
+    uint32_t o[16];
+    tmem_ld16(o_col + 16u * h, o);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+    tmem_st16(o_col + 16u * h, o);
+  }
+  return true;
+}
+
+// Rows r .. r + 31 of a CTA again, one by one: a warp's work, behind its own results.
+template <int D>
+__device__ __noinline__ void redo_rows(const Kv8Attn& p, int splits, float* part, float* qs, int64_t r) {
+  const int64_t b = blockIdx.z, hk = blockIdx.y, group = p.heads_q / p.c.heads;
+  const Span sp = sequence_span(p, b);
+  const int split = (int)blockIdx.x % splits, c = (threadIdx.x & 31) * (D / 32);
+  const int64_t rows = sp.nq * group, r0 = r / 256 * 256, end = min(rows, r + 32);
+  const KeyTiles kt = key_tiles(p, sp.pos((int)(r0 / group)), sp.pos((int)((min(rows, r0 + 256) - 1) / group)), 128);
+  const int i0 = (int)((int64_t)kt.n * split / splits), i1 = (int)((int64_t)kt.n * (split + 1) / splits);
+  __syncwarp();
+#pragma unroll 1
+  for (; r < end; ++r) {
+    const int64_t tok = r / group, hq = hk * group + r - tok * group;
+    ExactRow<D> row;
+    exact_row<D>(p, b, hk, tok, hq, sp.len, sp.pos((int)tok), kt, 128, i0, i1, qs, row);
+    if (splits == 1) {
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + b * p.os[0] + tok * p.os[1] +
+                                                  hq * p.os[2] + c);
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e)
+        dst[e] = pack_bf16x2(__float_as_uint(row.y[2 * e]), __float_as_uint(row.y[2 * e + 1]));
+      if (p.lse && c == 0) p.lse[(b * p.heads_q + hq) * p.n_q + tok] = row.lse2 * 0.6931471805599453f;
+    } else {
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) part_row(p, part, split, b, hk, r)[c + e] = row.y[e];
+      if (c == 0) *part_lse(p, part, splits, split, b, hk, r) = row.lse2;
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_kv8_tiles(const __grid_constant__ Kv8Attn p, int splits, float* part) {
   extern __shared__ uint8_t smem_raw[];
   if (p.prec && *p.prec == SB_SKIP) return;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -196,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
     }
     mbar_init(&sh.drain, 1);
     sh.abort = 0;
-    sh.evmax = 0;
+    sh.e0 = sh.redo = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
   }
@@ -253,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
         mbar_arrive(&sh.q_full);
       }
       const uint32_t s_col = tmem + lanes + kSCols * t, o_col = tmem + lanes + kOCol + (uint32_t)(D * t);
-      float m = -INFINITY, l = 0.0f;
+      RowStats st{-INFINITY, 0.0f, 0};
       bool ok = true;
       for (int u = 0; u < 2 * n; ++u) {
         const int buf = kBufs == 2 ? u & 1 : 0;
@@ -277,28 +325,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
 #pragma unroll
         for (int i = 0; i < 64; i += 2)
           mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-        const float mn = fmaxf(m, fmaf(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), c, te.v));
-        if (__any_sync(0xffffffffu, mn > m + kRise)) {
-          const float f = mn == m ? 1.0f : ex2(m - mn);
-          m = mn;
-          l *= f;
-          if (u > 0) {  // the accumulator is complete up to step u - 1 once that step's product is done; the
-                        // phase before is behind the scores just read, so the parity is not ambiguous
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.o_done[t], (uint32_t)((u - 1) & 1), abort, kWaitNs));
+        const float mn = fmaxf(st.m, fmaf(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), c, te.v));
+        if (__any_sync(0xffffffffu, mn > st.m + kRise)) {
+          const float f = mn == st.m ? 1.0f : fast_ex2(st.m - mn);
+          if (mn > st.m) move_max(st, mn, te.e);
+          if (u > 0) {
+            ok = rescale<D>(sh, t, u, o_col, f);
             if (!ok) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int h = 0; h < D / 16; ++h) {
-              uint32_t o[16];
-              tmem_ld16(o_col + 16u * h, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st16(o_col + 16u * h, o);
-            }
           }
         }
-        const float add = te.v + (float)kShift - (m == -INFINITY ? 0.0f : m);
+        const float add = te.v + (float)kShift - (st.m == -INFINITY ? 0.0f : st.m);
         const uint64_t cc = pack2(c, c), aa = pack2(add, add);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -308,8 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
           for (int i = 0; i < 32; i += 2) {
             float y0, y1;
             unpack2(fma2(pack2u(x[32 * h + i], x[32 * h + i + 1]), cc, aa), y0, y1);
-            y0 = ex2(y0);
-            y1 = ex2(y1);
+            y0 = fast_ex2(y0);
+            y1 = fast_ex2(y1);
             sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pack2(y0, y1));
             w[i / 2] = pack_f16(y0, y1);
           }
@@ -317,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
         }
         float s0, s1;
         unpack2(add2(sum[0], sum[1]), s0, s1);
-        l = fmaf(s0 + s1, te.iv, l);
+        st.l = fmaf(s0 + s1, sum_factor(st.e - te.e), st.l);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&sh.p_full[t][buf]);
@@ -329,8 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
       } else {
         tc_fence_after();
         // nothing visible: zeros and -inf; a NaN row has a NaN sum and stays NaN
-        const float inv = l > 0.0f ? kUnshift / l : l, unit = pow2_byte(sh.evmax);
-        const float lse2 = l > 0.0f ? m + log2f(l) : l == 0.0f ? -INFINITY : l;
+        const float inv = st.l > 0.0f ? 1.0f / st.l : st.l;
+        const float lse2 = st.l > 0.0f ? st.m - (float)st.e + log2f(st.l) : st.l == 0.0f ? -INFINITY : st.l;
+        const float2 unit = output_unit(st.e, sh.e0);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -342,8 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
             for (int i = 0; i < 32; ++i) o[i] = 0u;
           }
 #pragma unroll
-          for (int i = 0; i < 32; ++i)  // in this order no factor leaves the normal range
-            o[i] = __float_as_uint(__uint_as_float(o[i]) * inv * unit);
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * unit.x * inv * unit.y);
           if (!live) continue;
           if (splits == 1) {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + b * p.os[0] + tok * p.os[1] +
@@ -365,6 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
           else if (p.lse)
             p.lse[(b * p.heads_q + hq) * p.n_q + tok] = lse2 * 0.6931471805599453f;
         }
+        if (sh.redo) redo_rows<D>(p, splits, part, sh.q[warp], r0 + 32 * warp);
       }
     }
   } else if (warp < 12) {
@@ -377,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
     const uint8_t* vx = p.c.v_exp + head0 / 64;
     const int blocks = (sp.len + 63) >> 6;
     uint4 kreg[kPieces], vreg[kPieces];
-    int ke[2] = {127, 127}, ve[2] = {0, 0};  // exponent bytes of the next tile's blocks
+    int ke[2], ve[2], e0 = 0, most = 0;  // exponent bytes of the next tile's blocks; V's first and largest so far
     auto fetch = [&](const uint8_t* codes, int j, uint4 (&u)[kPieces]) {
       const int j0 = kt.tile(i0 + j) * 128;
       const uint8_t* src = codes + (head0 + j0) * D;
@@ -387,13 +424,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
         u[i] = j0 + tok < sp.len ? ldg_v4(src + (int64_t)q * 16) : make_uint4(0, 0, 0, 0);
       }
     };
-    auto fetch_exps = [&](int j) {  // a block past the end: any finite scale
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int blk = kt.tile(i0 + j) * 2 + h;
-        ke[h] = blk < blocks ? (int)kx[blk] : 127;
-        ve[h] = blk < blocks ? (int)vx[blk] : 0;
-      }
+    auto fetch_exps = [&](int j) {  // a tile's first block is never past the end; a second one that is: the first's
+      const int blk = kt.tile(i0 + j) * 2, next = blk + 1 < blocks ? blk + 1 : blk;
+      ke[0] = (int)kx[blk], ke[1] = (int)kx[next];
+      ve[0] = (int)vx[blk], ve[1] = (int)vx[next];
     };
     auto put = [&](uint32_t tile, const uint4 (&u)[kPieces]) {
 #pragma unroll
@@ -410,20 +444,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
     if (n > 0) {
       fetch(p.c.k_codes, 0, kreg);
       fetch_exps(0);
+      e0 = ve[0];
+      if (tid == 0) sh.e0 = e0;
       fetch(p.c.v_codes, 0, vreg);
     }
-    {  // the largest exponent of V over this CTA's tiles
-      int e = 0;
-      for (int i = tid; i < 2 * n; i += 128) {
-        const int blk = kt.tile(i0 + (i >> 1)) * 2 + (i & 1);
-        if (blk < blocks) e = max(e, (int)vx[blk]);
-      }
-#pragma unroll
-      for (int s = 16; s >= 1; s >>= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, s));
-      if (lane == 0) atomicMax(&sh.evmax, e);
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-    }
-    const int evmax = sh.evmax;
     for (int j = 0; ok && j < n; ++j) {
       const int s = j & 1;
       const uint32_t ph = (uint32_t)((j >> 1) & 1);
@@ -431,13 +455,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
         ok = false;
         break;
       }
-      const bool far[2] = {ve[0] < evmax - 64, ve[1] < evmax - 64};
+      // More than 2^64 below the largest so far, which no row's exponent passes: values of zero are then as good as
+      // theirs, unless they are not zero.
+      const int floor0 = max(most, ve[0]) - kFar, floor1 = max(most, max(ve[0], ve[1])) - kFar;
+      const bool far[2] = {ve[0] < floor0, ve[1] < floor1};
+      bool redo = false;
+      most = max(most, max(ve[0], ve[1]));
       if (tid < 2) {  // four tiles' worth: a softmax may still read those of tile j - 2 here
         TileExp& te = sh.exps[j & 3][tid];
-        const int rel = max((tid ? ve[1] : ve[0]) - evmax, -64);
         te.k = pow2_byte(tid ? ke[1] : ke[0]);
-        te.v = (float)rel;
-        te.iv = __uint_as_float((uint32_t)(127 - rel - kShift) << 23);
+        te.e = (tid ? max(ve[1], floor1) : max(ve[0], floor0)) - e0;
+        te.v = (float)te.e;
       }
       put(k_s + s * kOp, kreg);
       fence_proxy_async_smem();
@@ -450,9 +478,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_tiles(const Kv8Attn p, int 
         ok = false;
         break;
       }
+      if (far[0] || far[1]) {
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i)  // a block more than 2^64 below the largest counts as zero
-        if (far[i >= kPieces / 2]) vreg[i] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kPieces; ++i) {
+          if (!far[i >= kPieces / 2]) continue;
+          redo |= ((vreg[i].x | vreg[i].y | vreg[i].z | vreg[i].w) & 0x7f7f7f7fu) != 0;
+          vreg[i] = make_uint4(0, 0, 0, 0);
+        }
+      }
+      if (redo) sh.redo = 1;
       put(v_s + s * kOp, vreg);
       fence_proxy_async_smem();
       mbar_arrive(&sh.v_full[s]);
