@@ -544,8 +544,9 @@ typedef struct {
  * that n keys of less weight are lost up to n 2^-32 P. The row's sum and lse count every weight in full; all sums
  * are FP32. Scales of any spread are sound; a head whose values differ by more than 2^64 from block to block may
  * take some hundred times longer where there are more than 16 query rows for a key head. A NaN
- * that was stored (sb_kv8_store reports it) stays in its head of its sequence, but may reach queries there
- * that do not see it: a weight of zero times a NaN is one. Inference only: no gradient is computed.
+ * that was stored (sb_kv8_store reports it) makes its channel of the queries that see it NaN, in a key all channels,
+ * and reaches no others; a head with values from 1.75 * 2^127 on, which may be one, is slower in the same way.
+ * Inference only: no gradient is computed.
  * lens or q_lens out of range are clamped and SB_ESHAPE is reported by sb_check. ws_bytes: size of ws
  * (SB_ESHAPE if too small). */
 sb_status sb_kv8_attention(const void* q, const int64_t* q_strides, int64_t n_q, int64_t heads_q,

@@ -36,6 +36,13 @@ def attend(sb, p, q, causal=False, window=0, sinks=0, scale=None, nan=None):
     return ref, tol
 
 
+def refer(p):
+    """The reference takes over what the GPU's cache holds."""
+    g, r = p.gpu, p.ref
+    r.codes[0], r.codes[1], r.exps[0], r.exps[1] = npy(g.k_codes), npy(g.v_codes), npy(g.k_exp), npy(g.v_exp)
+    r.lens[:] = npy(g.lens)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("n", [1, 40, 300])
 @pytest.mark.parametrize("power", [-130, -126, -123, -119, -112])
@@ -161,3 +168,53 @@ def test_tokens_behind_the_window_leave_later_rows_alone(sbg, n):
     p.store(k, v.to(torch.bfloat16))
     for window, sinks in ((1, 0), (40, 0), (100, 3), (200, 70)):
         attend(sbg, p, heads(1, n, 2, 64, 3), causal=True, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,held,at", [(5, 130, 128), (16, 200, 193), (300, 448, 256), (300, 448, 300), (384, 448, 64)])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_a_nonfinite_value_reaches_only_what_sees_it(sbg, n, held, at, D, bad):
+    """Causal and windowed: a stored Inf (the code of its block's largest value) or NaN changes its own channel of
+    the rows that see it and nothing else."""
+    p = Pair(sbg, 1, 2, 512, D)
+    k, v = heads(1, held, 2, D, 1), heads(1, held, 2, D, 2)
+    v[0, at, 1, 7] = bad
+    sbg.kv8_store(k, v, p.gpu, ws=p.ws)
+    with pytest.raises(sbg.SixbitError):
+        sbg.check(p.ws)
+    refer(p)
+    nan = p.ref.codes[1] & 0x7f == 0x7f
+    nan[:, :, held:] = False
+    assert nan.sum() == (1 if bad != bad else 0)
+    p.ref.codes[1][nan] = 0
+    if bad == bad:  # 448 * 2^120 is past FP32: rows that see it may overflow, keep it below
+        p.gpu.v_exp[0, 1, at // 64] = 200
+        p.ref.exps[1][0, 1, at // 64] = 200
+    q = heads(1, n, 4, D, 3)
+    for window, sinks in ((0, 0), (60, 2)):
+        mark = None
+        if bad != bad:
+            mark = np.zeros((1, n, 4, D), bool)
+            see = ref8.visible(held, n, True, window, sinks)[:, at]
+            mark[0, see, 2:, 7] = True
+        attend(sbg, p, q, causal=True, window=window, sinks=sinks, nan=mark)
+
+
+def test_a_nonfinite_key_reaches_only_what_sees_it(sbg):
+    for n, held, at in ((5, 130, 128), (300, 448, 300)):
+        p = Pair(sbg, 1, 1, 512, 64)
+        k, v = heads(1, held, 1, 64, 1), heads(1, held, 1, 64, 2)
+        k[0, at, 0, 7] = float("nan")
+        sbg.kv8_store(k, v, p.gpu, ws=p.ws)
+        refer(p)
+        nan = p.ref.codes[0] & 0x7f == 0x7f
+        p.ref.codes[0][nan] = 0
+        q = heads(1, n, 1, 64, 3)
+        out = torch.empty_like(q)
+        ws = sbg.AttnWorkspace(1, 1, n, 64)
+        sbg.kv8_attention(q, p.gpu, out, causal=True, ws=ws)
+        sbg.check(ws)
+        ref, _, tol, _ = ref8_bound.attention(p.ref, ref8.f64(q), [n], 0.125, True)
+        got, sees = ref8.f64(out), ref8.visible(held, n, True, 0, 0)[:, at]
+        assert np.isnan(got[0, sees]).all()
+        assert (np.abs(got - ref)[0, ~sees] <= tol[0, ~sees]).all()

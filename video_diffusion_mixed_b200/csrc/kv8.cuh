@@ -144,6 +144,10 @@ __device__ __forceinline__ bool tile_needs_mask(const Kv8Attn& p, int j0, int si
          (p.window > 0 && pmax - j0 >= (int)p.window && j0 + size > (int)p.sinks);
 }
 
+// sb_kv8_store gives a block that holds a NaN or an Inf an exponent byte of at least this one (that of the largest
+// finite values, from 1.75 * 2^127 on). A weight of zero does not hide a NaN in the products.
+constexpr int kNanExp = 247;
+
 // One row by itself, a warp's work, in FP32 throughout: for what the kernels' products cannot hold. Values of keys that
 // the row does not see are not touched, so a NaN among them stays there. Rare, and some hundred times slower than the
 // tensor cores: a lane takes a key's score, then D / 32 channels of the output.

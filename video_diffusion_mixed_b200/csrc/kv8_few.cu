@@ -168,10 +168,39 @@ constexpr int few_smem() {
   return kFewWarps * kFewSlots * 2 * kStep * D + 1024 + kFewWarps * kFewSlots * 8;
 }
 
+// A share's rows again, one by one in FP32: its values may hold a NaN, which only rows that see it may meet. A warp
+// takes every fourth row.
+template <int D>
+__device__ __noinline__ void few_redo(const Kv8Attn& p, int64_t b, int64_t hk, KeyTiles kt, int i0, int i1, int tiles,
+                                      float* qs, float* part) {
+  const int lane = threadIdx.x & 31, c = lane * (D / 32);
+  const Span sp = sequence_span(p, b);
+  const int group = (int)(p.heads_q / p.c.heads), rows = sp.nq * group;
+#pragma unroll 1
+  for (int r = (int)threadIdx.x >> 5; r < rows; r += kFewWarps) {
+    const int64_t tok = r / group, hq = hk * group + r - tok * group;
+    ExactRow<D> row;
+    exact_row<D>(p, b, hk, tok, hq, sp.len, sp.pos((int)tok), kt, 64, i0, i1, qs, row);
+    if (i1 - i0 == tiles) {
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + b * p.os[0] + tok * p.os[1] +
+                                                  hq * p.os[2] + c);
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e)
+        dst[e] = pack_bf16x2(__float_as_uint(row.y[2 * e]), __float_as_uint(row.y[2 * e + 1]));
+      if (p.lse && lane == 0) p.lse[(b * p.heads_q + hq) * p.n_q + tok] = row.lse2 * 0.6931471805599453f;
+    } else {
+      const int side = i0 > 0 ? 0 : 1;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) few_part(part, D, blockIdx.x, side, r)[c + e] = row.y[e];
+      if (lane == 0) *few_part_lse(part, D, gridDim.x, blockIdx.x, side, r) = row.lse2;
+    }
+  }
+}
+
 // NT tiles of eight query rows. deal: the tiles are dealt out as above; otherwise a block takes one head.
 template <int D, int NT>
-__global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__ FewMaps tm, const Kv8Attn p, int deal,
-                                                         float* part) {
+__global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__ FewMaps tm,
+                                                         const __grid_constant__ Kv8Attn p, int deal, float* part) {
   extern __shared__ uint8_t few_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(few_smem_raw) + 1023) & ~(uintptr_t)1023);
   constexpr int kC = D / 64, kN = D / 8, kBox = kStep * D;
@@ -298,6 +327,7 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][n][e] = 0.0f;
 
+    bool redo = false;
     for (int q = warp; q < steps; q += kFewWarps) {
       const int blk = kt.tile(i0 + (q >> 1)), j0 = blk * 64 + (q & 1) * kStep;
       const int ke = (int)__ldg(kx + blk), ve = (int)__ldg(vx + blk);  // a tile starts below len
@@ -330,6 +360,7 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
         }
       }
       const int rel = ve - e0;
+      redo |= ve >= kNanExp;
       const float ev = (float)rel, ks = pow2_byte(ke);
       const bool mask = tile_needs_mask(p, j0, kStep, pmin, pmax);
       uint32_t w[2][NT][2];
@@ -438,7 +469,7 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int s = 4; s < 32; s <<= 1) st[n][e].l += __shfl_xor_sync(0xffffffffu, st[n][e].l, s);
-    __syncthreads();  // the ring's memory is reused
+    const bool again = __syncthreads_or(redo);  // the ring's memory is reused
     constexpr int kRows = 8 * NT;
     float* so = reinterpret_cast<float*>(smem);  // [warp][row][D + 4] outputs, then [warp][row] statistics
     RowStats* ss = reinterpret_cast<RowStats*>(so + kFewWarps * kRows * (D + 4));
@@ -455,7 +486,7 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
       }
     }
     __syncthreads();
-    for (int i = tid; i < rows * (D / 4); i += kFewThreads) {
+    for (int i = again ? rows * (D / 4) : tid; i < rows * (D / 4); i += kFewThreads) {
       const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
       RowStats all{-INFINITY, 0.0f, 0};
 #pragma unroll
@@ -500,6 +531,7 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
         if (c == 0) *few_part_lse(part, D, gridDim.x, blockIdx.x, side, r) = lse2;
       }
     }
+    if (again) few_redo<D>(p, b, hk, kt, i0, i1, tiles, reinterpret_cast<float*>(ss + kFewWarps * kRows) + warp * D, part);
     at += i1 - i0;
     if (!deal || at >= at_end) break;
     fence_proxy_async_smem();  // the join's memory is the ring's again
@@ -626,7 +658,7 @@ static bool cache_map(CUtensorMap* m, const uint8_t* base, const sb_kv8& c) {
 template <int D, int NT>
 static cudaError_t launch_few(const Kv8Attn& p, int deal, unsigned grid, float* part, cudaStream_t s) {
   constexpr int kBytes = few_smem<D>() + 1024;  // + alignment of the dynamic base
-  static_assert(kFewSlots * kFewWarps * 2 * kStep * D >= kFewWarps * 8 * NT * ((int)sizeof(RowStats) + 4 * (D + 4)),
+  static_assert(kFewSlots * kFewWarps * 2 * kStep * D >= kFewWarps * (8 * NT * ((int)sizeof(RowStats) + 4 * (D + 4)) + 4 * D),
                 "the join fits the ring");
   static std::atomic<uint64_t> attr{0};
   const cudaError_t e = smem_attr_once(k_kv8_few<D, NT>, kBytes, attr);

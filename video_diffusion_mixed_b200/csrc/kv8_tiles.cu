@@ -12,8 +12,8 @@
 // fp16 operands once for the 256 rows. The block scales are powers of two and never touch the tiles:
 // the keys' enters c, the values' exponent ev the exponent of w, and with it the running maximum, which is
 // that of what w V sums; the row sum takes it out again by an exact factor (RowStats in kv8.cuh). A block of
-// values 2^64 below the largest before it is left out of the product, and if it holds anything but zeros the
-// CTA computes its rows again one by one in FP32: a branch for that in the softmax's loop, taken or not, cost a
+// values 2^64 below the largest before it is left out of the product, and if it holds anything but zeros, or if
+// a block may hold a NaN, the CTA computes its rows again one by one in FP32: a branch for that in the softmax's loop, taken or not, cost a
 // tenth of the time of 17776 x 17776, a second loop behind it as much. Queries are scaled by a power of two to
 // [2^14, 2^15) and rounded to fp16, exact for every component within 2^-31 of the row's largest. The maximum
 // moves only when it would rise by more than 2^8, so the accumulator is rescaled rarely; the rest of fp16's
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // theirs, unless they are not zero.
       const int floor0 = max(most, ve[0]) - kFar, floor1 = max(most, max(ve[0], ve[1])) - kFar;
       const bool far[2] = {ve[0] < floor0, ve[1] < floor1};
-      bool redo = false;
+      bool redo = max(ve[0], ve[1]) >= kNanExp;
       most = max(most, max(ve[0], ve[1]));
       if (tid < 2) {  // four tiles' worth: a softmax may still read those of tile j - 2 here
         TileExp& te = sh.exps[j & 3][tid];
