@@ -218,3 +218,17 @@ def test_a_nonfinite_key_reaches_only_what_sees_it(sbg):
         got, sees = ref8.f64(out), ref8.visible(held, n, True, 0, 0)[:, at]
         assert np.isnan(got[0, sees]).all()
         assert (np.abs(got - ref)[0, ~sees] <= tol[0, ~sees]).all()
+
+
+def test_one_workspace_for_a_prompt_and_its_tokens(sbg):
+    """Sized for the longest prompt of the largest batch: shorter prompts, single tokens and smaller batches fit."""
+    ws = sbg.AttnWorkspace(2, 32, 9000, 64)
+    for B, n, Hq, H in ((2, 9000, 32, 2), (2, 700, 8, 2), (1, 40, 32, 1), (2, 1, 32, 2), (1, 3, 4, 4)):
+        p = Pair(sbg, B, H, 9024, 64)
+        p.fill([9000] + [5000] * (B - 1), seed=9)
+        q = heads(B, n, Hq, 64, 10)
+        out, own = torch.empty_like(q), torch.empty_like(q)
+        sbg.kv8_attention(q, p.gpu, out, causal=True, ws=ws)
+        sbg.check(ws)
+        sbg.kv8_attention(q, p.gpu, own, causal=True, ws=sbg.AttnWorkspace(B, Hq, n, 64))
+        assert torch.equal(out, own)

@@ -1077,8 +1077,6 @@ sb_status sb_kv8_attention(const void* q, const int64_t* q_strides, int64_t n_q,
       (st = check_strides(out_strides, n_q, heads_q, cache->batch, "out")) != SB_OK || (st = check_prec(prec)) != SB_OK)
     return st;
   SB_REQUIRE((reinterpret_cast<uintptr_t>(q_lens) & 3u) == 0, SB_EALIGN, "q_lens misaligned");
-  const size_t need = sb::kv8_workspace_bytes(cache->batch, heads_q, n_q, cache->dim);
-  SB_REQUIRE(ws_bytes >= need, SB_ESHAPE, "ws holds %zu bytes, %zu are needed", ws_bytes, need);
   sb::Kv8Attn p{};
   p.c = *cache;
   p.q = q;
@@ -1095,8 +1093,11 @@ sb_status sb_kv8_attention(const void* q, const int64_t* q_strides, int64_t n_q,
   p.lse = lse;
   p.prec = prec;
   p.hdr = static_cast<sb::WsHeader*>(ws);
+  const sb::Kv8Plan plan = sb::kv8_plan(p);
+  SB_REQUIRE(ws_bytes >= plan.bytes, SB_ESHAPE, "ws holds %zu bytes, %zu are needed", ws_bytes, plan.bytes);
   const char* why = "";
-  cudaError_t e = sb::launch_kv8_attention(p, static_cast<char*>(ws) + sb::kKv8PartOffset, (cudaStream_t)stream, &why);
+  cudaError_t e = sb::launch_kv8_attention(p, plan, static_cast<char*>(ws) + sb::kKv8PartOffset, (cudaStream_t)stream,
+                                           &why);
   if (e != cudaSuccess) return cuda_fail(e, why);
   return ok();
 }

@@ -24,6 +24,8 @@
 // bound by the boxes in flight (DRAM at 64 percent) and by the start and the join, 8 us of the 54.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
+
 #include "kv8.cuh"
 #include "launch_util.h"
 #include "sb_device.cuh"
@@ -678,13 +680,15 @@ static int few_blocks(int dim) { return dim == 64 ? 592 : 296; }
 // Many rows: the number of parts of the keys with the shortest schedule of 148 CTAs; a part costs its key
 // tiles and about six more (10 us) for its start and its end, and its results two passes over memory. 1350
 // tokens of 30 heads of 64 that see 11026 keys: 1 / 2 / 3 / 4 / 6 / 8 parts took 332 / 289 / 281 / 284 / 312 / 338 us.
+constexpr int kMaxSplits = 16;
+constexpr int64_t kPartBytes = (int64_t)128 << 20;  // of partial outputs, at most
 static int plan_splits(int64_t batch, int64_t heads, int64_t heads_q, int64_t n_q, int dim, int64_t keys) {
   const int64_t rows = n_q * (heads_q / heads), tiles = ceil_div(rows, 256) * batch * heads, len = ceil_div(keys, 128);
-  const int64_t most = ((int64_t)128 << 20) / (batch * n_q * heads_q * dim * 4);  // 128 MB of partial results
+  const int64_t most = kPartBytes / (batch * n_q * heads_q * dim * 4);
   const int64_t join = batch * n_q * heads_q * dim * 4 / 400000;                  // of a part, in 1/16 key tiles (0.1 us)
   int best = 1;
   int64_t cost = ceil_div(tiles, 148) * (len * 16 + 96);
-  for (int s = 2; s <= 16 && s <= most && s * 4 <= len; ++s) {
+  for (int s = 2; s <= kMaxSplits && s <= most && s * 4 <= len; ++s) {
     const int64_t c = ceil_div(tiles * s, 148) * (len * 16 / s + 96) + 40 + s * join;
     if (c < cost) cost = c, best = s;
   }
@@ -693,14 +697,31 @@ static int plan_splits(int64_t batch, int64_t heads, int64_t heads_q, int64_t n_
 
 }  // namespace kv8
 
-cudaError_t launch_kv8_attention(const Kv8Attn& p, void* part_, cudaStream_t s, const char** why) {
+Kv8Plan kv8_plan(const Kv8Attn& p) {
+  using namespace kv8;
+  Kv8Plan plan{p.n_q * (p.heads_q / p.c.heads) <= kFewRows, false, 1, kKv8PartOffset};
+  int64_t floats = 0;
+  if (plan.few) {
+    plan.deal = p.c.batch * p.c.heads < kFewUnits;
+    if (plan.deal) floats = (int64_t)few_blocks(p.c.dim) * 2 * kFewRows * (p.c.dim + 1);
+  } else {
+    int64_t keys = p.c.capacity;
+    if (p.window > 0 && p.window + p.sinks + p.n_q < keys) keys = p.window + p.sinks + p.n_q;
+    plan.splits = plan_splits(p.c.batch, p.c.heads, p.heads_q, p.n_q, p.c.dim, keys);
+    if (plan.splits > 1) floats = plan.splits * part_rows(p) * (p.c.dim + 1);
+  }
+  plan.bytes += (size_t)(floats * 4 + 15) / 16 * 16;
+  return plan;
+}
+
+cudaError_t launch_kv8_attention(const Kv8Attn& p, const Kv8Plan& plan, void* part_, cudaStream_t s, const char** why) {
   using namespace kv8;
   *why = "sb_kv8_attention";
   float* part = static_cast<float*>(part_);
-  const int64_t rows = p.n_q * (p.heads_q / p.c.heads), units = p.c.batch * p.c.heads, all = part_rows(p);
-  if (rows <= kFewRows) {
-    const int deal = units < kFewUnits;
-    const unsigned grid = deal ? (unsigned)few_blocks(p.c.dim) : (unsigned)units;
+  const int64_t rows = p.n_q * (p.heads_q / p.c.heads), all = part_rows(p);
+  if (plan.few) {
+    const int deal = plan.deal;
+    const unsigned grid = deal ? (unsigned)few_blocks(p.c.dim) : (unsigned)(p.c.batch * p.c.heads);
     cudaError_t e;
     if (p.c.dim == 64)
       e = rows <= 8 ? launch_few<64, 1>(p, deal, grid, part, s) : launch_few<64, 2>(p, deal, grid, part, s);
@@ -712,9 +733,7 @@ cudaError_t launch_kv8_attention(const Kv8Attn& p, void* part_, cudaStream_t s, 
     return p.c.dim == 64 ? cudaLaunchKernelEx(&L.cfg, k_kv8_join_few<64>, p, (int)grid, part)
                          : cudaLaunchKernelEx(&L.cfg, k_kv8_join_few<128>, p, (int)grid, part);
   }
-  int64_t keys = p.c.capacity;
-  if (p.window > 0 && p.window + p.sinks + p.n_q < keys) keys = p.window + p.sinks + p.n_q;
-  const int splits = plan_splits(p.c.batch, p.c.heads, p.heads_q, p.n_q, p.c.dim, keys);
+  const int splits = plan.splits;
   const cudaError_t e = launch_kv8_tiles(p, splits, part, s, why);
   if (e != cudaSuccess || splits == 1) return e;
   *why = "sb_kv8_attention (join)";
@@ -723,21 +742,18 @@ cudaError_t launch_kv8_attention(const Kv8Attn& p, void* part_, cudaStream_t s, 
                        : cudaLaunchKernelEx(&L.cfg, k_kv8_join<128>, p, splits, part);
 }
 
-// The most that any number of key heads and any capacity need.
+// What any call of at most these sizes may need, whatever its key heads, capacity and window. A smaller call may
+// need more than a larger one (it is split where the larger one fills the chip), so this is a bound over all of
+// them: the dealt-out parts of a few rows, which a single token of a single sequence needs already, and as many parts
+// of many rows as kMaxSplits and kPartBytes allow.
 size_t kv8_workspace_bytes(int64_t batch, int64_t heads_q, int64_t n_q, int dim) {
-  int64_t most = 0;  // floats
-  for (int64_t heads = 1; heads <= heads_q; ++heads) {
-    if (heads_q % heads) continue;
-    int64_t f = 0;
-    if (n_q * (heads_q / heads) <= kv8::kFewRows) {
-      if (batch * heads < kv8::kFewUnits) f = (int64_t)kv8::few_blocks(dim) * 2 * kv8::kFewRows * (dim + 1);
-    } else {
-      const int64_t s = kv8::plan_splits(batch, heads, heads_q, n_q, dim, (int64_t)1 << 30);
-      if (s > 1) f = s * batch * n_q * heads_q * (dim + 1);
-    }
-    if (f > most) most = f;
+  using namespace kv8;
+  int64_t floats = (int64_t)few_blocks(dim) * 2 * kFewRows * (dim + 1);
+  if (n_q * heads_q > kFewRows) {
+    const int64_t rows = batch * n_q * heads_q, most = kPartBytes / (dim * 4);
+    floats = std::max(floats, std::min(kMaxSplits * rows, most) * (dim + 1));
   }
-  return kKv8PartOffset + (size_t)(most * 4 + 15) / 16 * 16;
+  return kKv8PartOffset + (size_t)(floats * 4 + 15) / 16 * 16;
 }
 
 }  // namespace sb

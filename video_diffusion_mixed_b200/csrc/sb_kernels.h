@@ -229,7 +229,14 @@ struct Kv8Attn {
 };
 cudaError_t launch_kv8_store(const Kv8Store& p, cudaStream_t s);
 constexpr size_t kKv8PartOffset = 256;  // partial results in the attention workspace, behind the header
-cudaError_t launch_kv8_attention(const Kv8Attn& p, void* part, cudaStream_t s, const char** why);
+struct Kv8Plan {
+  bool few;    // the streaming kernel for few query rows ...
+  bool deal;   // ... with the tiles dealt out
+  int splits;  // parts of the keys in the tensor-core kernel
+  size_t bytes;  // of workspace
+};
+Kv8Plan kv8_plan(const Kv8Attn& p);
+cudaError_t launch_kv8_attention(const Kv8Attn& p, const Kv8Plan& plan, void* part, cudaStream_t s, const char** why);
 cudaError_t launch_kv8_tiles(const Kv8Attn& p, int splits, float* part, cudaStream_t s, const char** why);
 size_t kv8_workspace_bytes(int64_t batch, int64_t heads_q, int64_t n_q, int dim);
 
