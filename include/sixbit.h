@@ -411,7 +411,7 @@ sb_status sb_delta_split(const void* X, int64_t M, int64_t K, const sb_cubes* cu
 
 /* Y [M][N] bf16 = act(Y_delta[t] + Y_core[cube(t)]) with Y_delta FP32 [M][N] and Y_core FP32
  * [ncube][N] (the core GEMM's output, which carries the bias); epilogue SB_EPI_NONE or
- * SB_EPI_GELU_TANH (tanh GELU with the hardware tanh approximation). N % 8 == 0. */
+ * SB_EPI_GELU_TANH (tanh GELU with the hardware tanh approximation: off by about 2^-12 of |v|). N % 8 == 0. */
 sb_status sb_delta_combine(const float* y_delta, const float* y_core, int64_t M, int64_t N,
                            const sb_cubes* cubes /* host */, int32_t epilogue, void* Y, sb_stream stream);
 
@@ -486,8 +486,8 @@ sb_status sb_prepare_weight_fp8(const void* W, const void* bias, int64_t N, int6
 /* Y [M][N] = act(X W^T + bias) with both operands in FP8 and FP32 accumulation. With X given (bf16
  * [M][K]) the call encodes X into `a` first, as sb_fp8_encode does; with X NULL it multiplies the
  * codes that `a` holds (one encode then serves several layers). epilogue SB_EPI_NONE or
- * SB_EPI_GELU_TANH; out_dtype SB_OUT_BF16 or SB_OUT_F32; M in [1, 2^30]. Y must not overlap X, `a`
- * or the weight. */
+ * SB_EPI_GELU_TANH (computed to some 2^-18 of the value, the negative tail included); out_dtype SB_OUT_BF16
+ * or SB_OUT_F32; M in [1, 2^30]. Y must not overlap X, `a` or the weight. */
 sb_status sb_linear_fp8(const void* X, const sb_fp8* a /* host */, const int32_t* prec,
                         const sb_weight_fp8* w /* host */, int32_t epilogue, int32_t out_dtype, void* Y, int64_t M,
                         void* ws, sb_stream stream);

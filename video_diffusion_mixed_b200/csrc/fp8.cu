@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kRowThreads) k_fp8_rows(Fp8Linear p) {
 #pragma unroll
   for (int w = 0; w < kRowWarps; ++w) y += red[w][m][r];
   if (p.bias) y += __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[n0 + r]);
-  if (p.epilogue == SB_EPI_GELU_TANH) y = gelu_tanh2(make_float2(y, 0.0f)).x;
+  if (p.epilogue == SB_EPI_GELU_TANH) y = gelu_exp2(make_float2(y, 0.0f)).x;
   const int64_t o = (int64_t)m * p.N + n0 + r;
   if (p.out_dtype == SB_OUT_F32)
     static_cast<float*>(p.Y)[o] = y;

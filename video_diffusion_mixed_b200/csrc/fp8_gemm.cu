@@ -191,7 +191,7 @@ __device__ __forceinline__ void finish32(const Params& p, const Bias32& o, uint3
     const float2 bias =
         p.bias ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)) : make_float2(0.0f, 0.0f);
     float2 y = ep_add2(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), bias);
-    if (p.gelu) y = gelu_tanh2(y);
+    if (p.gelu) y = gelu_exp2(y);
     r[2 * j] = __float_as_uint(y.x);
     r[2 * j + 1] = __float_as_uint(y.y);
   }

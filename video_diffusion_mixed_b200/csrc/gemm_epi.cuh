@@ -41,14 +41,28 @@ __device__ __forceinline__ float2 ep_add2(float2 a, float2 b) {
 }
 
 // tanh-form GELU, 0.5 v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))), with the SFU's tanh
-// approximation (relative error about 2^-11, below the 2^-9 rounding of the bf16 output), on two
-// values at a time.
+// approximation, on two values at a time. Its error (relative about 2^-11) is absolute in the result, about
+// 2^-12 |v|: below the bf16 rounding for positive v, but up to a fifth of the value at v = -3 and more
+// beyond, where the two terms cancel.
 __device__ __forceinline__ float2 gelu_tanh2(float2 v) {
   const float2 c1 = make_float2(0.7978845608028654f * 0.044715f, 0.7978845608028654f * 0.044715f);
   const float2 c0 = make_float2(0.7978845608028654f, 0.7978845608028654f);
   const float2 u = ep_mul2(v, ep_fma2(c1, ep_mul2(v, v), c0));
   const float2 h = ep_mul2(make_float2(0.5f, 0.5f), v);
   return ep_fma2(h, make_float2(tanh_approx(u.x), tanh_approx(u.y)), h);
+}
+
+// The same GELU as v / (1 + 2^(-2 log2(e) sqrt(2/pi) (v + 0.044715 v^3))), whose relative error stays near
+// 2^-20 in the negative tail: an exponential and a reciprocal for the tanh.
+__device__ __forceinline__ float2 gelu_exp2(float2 v) {
+  constexpr float kA = -2.0f * 1.4426950408889634f * 0.7978845608028654f;
+  const float2 a = ep_mul2(v, ep_fma2(make_float2(kA * 0.044715f, kA * 0.044715f), ep_mul2(v, v), make_float2(kA, kA)));
+  float ex, ey, rx, ry;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ex) : "f"(a.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ey) : "f"(a.y));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rx) : "f"(1.0f + ex));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ry) : "f"(1.0f + ey));
+  return make_float2(v.x * rx, v.y * ry);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
