@@ -131,7 +131,10 @@ constexpr int kRowSlots = 4;
 __global__ void __launch_bounds__(kRowThreads) k_fp8_rows(Fp8Linear p) {
   __shared__ uint4 wbuf[kRowSlots][4][kRowThreads];  // piece 2c + r: chunk c (64 channels), weight row g + 8r
   __shared__ float red[kRowWarps][8][17];
-  if (p.prec && *p.prec == SB_SKIP) return;
+  if (p.prec && *p.prec == SB_SKIP) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int K = (int)p.K, M = (int)p.M, nkb = (K + 127) / 128, groups = (K + 511) / 512;
   const int64_t n0 = (int64_t)blockIdx.x * 16;

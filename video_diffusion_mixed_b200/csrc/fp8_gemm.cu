@@ -300,7 +300,10 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   r.abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  if (p.prec && *p.prec == SB_SKIP) return;  // uniform over the grid
+  if (p.prec && *p.prec == SB_SKIP) {  // uniform over the grid
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
   const bool leader = rank == 0;

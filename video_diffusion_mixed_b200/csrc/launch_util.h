@@ -31,6 +31,8 @@ inline int device_sm_count() {
 // Launch configuration of a kernel that may start while the launch before it still runs (`early`):
 // the kernel calls griddepcontrol.wait before it touches what that launch writes. Only for a launch
 // that the library itself put in front, which in turn started after everything before it had ended.
+// Every block waits before it leaves, even one with nothing to do: what follows in the stream may start at this
+// launch's end, which must not come before that of the launch in front.
 struct LaunchAfter {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
