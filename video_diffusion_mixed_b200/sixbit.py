@@ -596,7 +596,7 @@ class WeightFp8:
 
     def __init__(self, W: torch.Tensor, bias: torch.Tensor | None = None, ws: Workspace | None = None, stream=None):
         N, K = W.shape
-        _dev(W.get_device(), bias)
+        _dev(W.get_device(), bias, ws and ws.buf)
         _typed(W, torch.bfloat16, (N, K), "W")
         _typed(bias, torch.bfloat16, (N,), "bias")
         self.N, self.K, self.bias = N, K, bias
@@ -614,7 +614,7 @@ class WeightFp8:
 def fp8_encode(X, a: Fp8Tensor, ws: Workspace, prec=None, stream=None):
     """sb_fp8_encode: the codes and scales of X [M, K] bf16 into a."""
     M, K = X.shape
-    _dev(X.get_device(), a.codes, prec)
+    _dev(X.get_device(), a.codes, prec, ws.buf)
     _typed(X, torch.bfloat16, (M, K), "X")
     _ck(lib().sb_fp8_encode(_ptr(X), M, K, _ptr(prec), ctypes.byref(a.c()), ws.ptr, _stream(stream)))
 
