@@ -23,7 +23,7 @@ LIB = os.path.join(HERE, "libsixbit.so")
 SOURCES = ["api.cu", "prepass.cu", "decide.cu", "gemm.cu", "prepass_static.cu", "reuse.cu", "chunks.cu", "delta.cu",
            "fp8.cu", "fp8_gemm.cu", "kv8.cu", "kv8_few.cu", "kv8_tiles.cu"]
 HEADERS = ["sb_device.cuh", "sb_kernels.h", "rows.cuh", "prepass_blk.cuh", "tmap.h", "launch_util.h", "gemm_epi.cuh",
-           "kv8.cuh"]
+           "kv8.cuh", "e4m3.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC,-O2,-Wall",

@@ -1,28 +1,11 @@
 // fp8.cu -- linear layer in 8-bit floating point: E4M3 codes with one E8M0 scale per 128 channels.
+#include "e4m3.cuh"
 #include "gemm_epi.cuh"
 #include "launch_util.h"
 #include "sb_device.cuh"
 #include "sb_kernels.h"
 
 namespace sb {
-
-// Exponent byte of a block with largest magnitude a, given as bf16 bits: the smallest e with
-// a <= 448 * 2^e (448 = 1.75 * 2^8), plus 127; a is 1.m * 2^(field - 127). Subnormal and zero a
-// give 0.
-__device__ __forceinline__ uint32_t e8m0_of_amax(uint32_t bits) {
-  const int b = (int)(bits >> 7) - 8 + ((bits & 0x7fu) > 0x60u ? 1 : 0);
-  return (uint32_t)max(b, 0);
-}
-
-// 2^-e for an exponent byte e + 127 (byte <= 253, which every finite bf16 amax gives).
-__device__ __forceinline__ float e8m0_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
-
-__device__ __forceinline__ uint32_t cvt_e4m3x4(float a, float b, float c, float d) {
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-  return (uint32_t)lo | ((uint32_t)hi << 16);
-}
 
 // One warp per (row, 512 channels): a lane takes 16 channels (two 16-byte loads, one 16-byte store of codes),
 // eight lanes a block, whose maximum takes three shuffles; four blocks make one 32-bit word of scales. Rows past
@@ -87,22 +70,6 @@ cudaError_t launch_fp8_encode(const void* X, int64_t M, int64_t K, const int32_t
 // ------------------------------------------------------------------------------------------------
 // Few rows (M <= 8): a stream over the weight
 // ------------------------------------------------------------------------------------------------
-
-// E4M3 pairs -> fp16 pairs, exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t b) {
-  uint32_t h;
-  const uint16_t in = (uint16_t)b;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(in));
-  return h;
-}
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 // 2^(a + b - 254) as two factors, so that no product in between leaves the range of FP32 when the
 // result does not.
@@ -194,8 +161,8 @@ __global__ void __launch_bounds__(kRowThreads) k_fp8_rows(Fp8Linear p) {
             const uint32_t a = i == 0 ? wa.x : i == 1 ? wa.y : i == 2 ? wa.z : wa.w;
             const uint32_t b = i == 0 ? wb.x : i == 1 ? wb.y : i == 2 ? wb.z : wb.w;
             const uint32_t y = i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w;
-            mma_f16(acc, e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(b), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(b >> 16),
-                    e4m3x2_to_f16x2(y), e4m3x2_to_f16x2(y >> 16));
+            mma_16816(acc, e4m3x2_f16x2(a), e4m3x2_f16x2(b), e4m3x2_f16x2(a >> 16), e4m3x2_f16x2(b >> 16),
+                    e4m3x2_f16x2(y), e4m3x2_f16x2(y >> 16));
           }
         }
         const int sh = 8 * (kb & 3);

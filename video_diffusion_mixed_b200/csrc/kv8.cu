@@ -1,28 +1,17 @@
 // kv8.cu -- FP8 key/value cache: the store of new tokens.
+#include "e4m3.cuh"
 #include "launch_util.h"
 #include "sb_device.cuh"
 #include "sb_kernels.h"
 
 namespace sb {
 
-__device__ __forceinline__ uint32_t kv_e8m0(uint32_t bits) {
-  return (uint32_t)max((int)(bits >> 7) - 8 + ((bits & 0x7fu) > 0x60u ? 1 : 0), 0);
-}
-__device__ __forceinline__ float kv_pow2(int byte) {  // 2^(byte - 127)
-  return byte <= 0 ? 0x1p-127f : __uint_as_float((uint32_t)byte << 23);
-}
-__device__ __forceinline__ uint32_t kv_codes4(float a, float b, float c, float d) {
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-  return (uint32_t)lo | ((uint32_t)hi << 16);
-}
-
 constexpr int kKvBlock = 64;  // positions that share a scale
 
 // An item is one cache block (64 positions) of the keys or the values of one head of one sequence, taken
 // by 128 threads; neighbouring items are the heads of the same tokens, whose rows lie next to one another
-// in k and v. Bound by memory: each new element is read once (2 bytes) and written once (1 byte). A thread
+// in k and v. Each new element is read once (2 bytes) and written once (1 byte); DRAM is at two fifths of its
+// rate, since a block has no load in flight while its warps meet and write. A thread
 // keeps its share of the item's new elements (at most 64 x 128 / 128 = 64 of them, 8 at a time) in registers
 // between the maximum and the codes. An item owns its positions and their exponent, so no two write the
 // same bytes. Blocks loop over the items: one ticket an item (for the lengths, below) cost more than the
@@ -90,9 +79,9 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv8_store(Kv8Store p, int64_t
     const int old = first > 0 ? *ep : 0;  // before the barrier: thread 0 writes it below
     __syncthreads();                      // two sets of maxima in turn: one barrier an item
     a = max(max(red[turn][0], red[turn][1]), max(red[turn][2], red[turn][3]));
-    const int need = (int)kv_e8m0(a);
+    const int need = (int)e8m0_of_amax(a);
     const int e8 = first > 0 ? max(old, need) : need;
-    const float inv = __uint_as_float((254u - (uint32_t)e8) << 23);
+    const float inv = e8m0_inverse((uint32_t)e8);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = threadIdx.x + kStoreThreads * i, tok = e / kVec;
@@ -100,18 +89,18 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv8_store(Kv8Store p, int64_t
       if (tok >= first && tok < last) {
         float v[8];
         unpack8(u[i], v);
-        *dst = make_uint2(kv_codes4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                          kv_codes4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+        *dst = make_uint2(cvt_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                          cvt_e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
       } else if (tok < first && e8 > old) {  // earlier tokens of the block, to the larger exponent
         const uint2 c = *dst;
-        const float f = kv_pow2(127 + old - e8);
+        const float f = pow2_byte(127 + old - e8);
         float v[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           v[j] = e4m3_to_f32(c.x >> (8 * j)) * f;
           v[4 + j] = e4m3_to_f32(c.y >> (8 * j)) * f;
         }
-        *dst = make_uint2(kv_codes4(v[0], v[1], v[2], v[3]), kv_codes4(v[4], v[5], v[6], v[7]));
+        *dst = make_uint2(cvt_e4m3x4(v[0], v[1], v[2], v[3]), cvt_e4m3x4(v[4], v[5], v[6], v[7]));
       }
     }
     if (threadIdx.x == 0) {

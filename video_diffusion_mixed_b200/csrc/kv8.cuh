@@ -4,18 +4,13 @@
 
 #include <cuda_fp16.h>
 
+#include "e4m3.cuh"
 #include "sb_device.cuh"
 #include "sb_kernels.h"
 
 namespace sb {
 namespace kv8 {
 
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t b) {  // exact
-  uint32_t h;
-  const uint16_t in = (uint16_t)b;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(in));
-  return h;
-}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -26,10 +21,6 @@ __device__ __forceinline__ uint32_t pack_bf16x2(uint32_t lo, uint32_t hi) {  // 
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
   return r;
 }
-__device__ __forceinline__ float pow2_byte(int byte) {  // 2^(byte - 127)
-  return byte <= 0 ? 0x1p-127f : __uint_as_float((uint32_t)byte << 23);
-}
-
 // A softmax weight is rounded to fp16 times 2^kShift: relative to the running maximum it is 2^kRise at most
 // before the maximum moves, 2^(kRise + kShift) stays in fp16's range, and the smallest weights, of which a long
 // cache has many, are rounded at 2^-(25 + kShift) of the largest. A rise of 4 and a shift of 11 would keep

@@ -17,11 +17,11 @@
 //
 // Block scales, the running maximum and its rare moves are those of the tensor-core kernel beside it.
 //
-// Measured (32 query heads, 8 key heads of 128, one token): 131071 tokens of one sequence 54 us (4.9 TB/s, the
+// Measured (32 query heads, 8 key heads of 128, one token): 131071 tokens of one sequence 56 us (4.8 TB/s, the
 // join included), 32 sequences of 8191 tokens 95 us (5.7 TB/s), of 1 to 8191 tokens 75; 30 heads of 64, 17776
 // tokens 24 us. A block a head, with no join, takes 86 us for the 32 equal sequences but 84 for the mixed ones
-// (the longest block sets the time) and leaves most of the chip idle with few sequences. A long cache is
-// bound by the boxes in flight (DRAM at 64 percent) and by the start and the join, 8 us of the 54.
+// (the longest block sets the time) and leaves most of the chip idle with few sequences. A long cache's
+// stream runs at 5.6 TB/s; the start and the join are 8 us of the 56.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -42,13 +42,6 @@ constexpr int kStep = 32;  // tokens
 constexpr uint64_t kFewWaitNs = 2000000000ull;  // far above any legitimate wait
 constexpr uint64_t kFewDrainNs = 20000000ull;
 
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {  // 8 x 8 matrix of 16-bit values
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
@@ -677,7 +670,8 @@ static cudaError_t launch_few(const Kv8Attn& p, int deal, unsigned grid, float* 
 constexpr int64_t kFewUnits = 1184;
 static int few_blocks(int dim) { return dim == 64 ? 592 : 296; }
 
-// Many rows: the number of parts of the keys with the shortest schedule of 148 CTAs; a part costs its key
+// Many rows: the number of parts of the keys, as many as the capacity and the window allow (the lengths are on the
+// device), with the shortest schedule of 148 CTAs; a part costs its key
 // tiles and about six more (10 us) for its start and its end, and its results two passes over memory. 1350
 // tokens of 30 heads of 64 that see 11026 keys: 1 / 2 / 3 / 4 / 6 / 8 parts took 332 / 289 / 281 / 284 / 312 / 338 us.
 constexpr int kMaxSplits = 16;
