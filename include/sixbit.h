@@ -237,7 +237,8 @@ sb_status sb_chunk_records(const void* X, int64_t M, int64_t K, int32_t block, f
  *   INT8:  Y = acc * s_x[m] * s_w[n] / B + bias, acc exact int32 (kind::i8);
  *   BF16:  Y = X W^T + bias on the raw X and original W (kind::f16), the PDR path.
  * The kind is read from *prec on the device (SB_SKIP: nothing is written). 1/B undoes the
- * unnormalised rotation of both operands. epilogue SB_EPI_GELU_TANH applies the tanh GELU.
+ * unnormalised rotation of both operands. epilogue SB_EPI_GELU_TANH applies the tanh GELU (hardware
+ * tanh: off by about 2^-12 of the argument).
  * out_dtype: SB_OUT_BF16 / SB_OUT_F32 write the result; SB_OUT_RAW writes the raw accumulator
  * (int32 for INT8, FP32 otherwise; test hook). X (bf16 [M][K]) may be NULL if the BF16 path is
  * never taken; a4/a8 may be NULL if that precision is never taken (the kernel then reports

@@ -27,11 +27,12 @@
 // ready. With heads of 128 there is one. Every wait is bounded (SB_ETIMEOUT).
 //
 // Measured: 17776 tokens of 30 heads of 64 over 17776 keys 3.4 ms (710 TFLOP/s); 8192 over 8192 of 8 heads of 128
-// 870 TFLOP/s, 980 with whole waves of CTAs. Bound by the exponentials (16 a clock and SM, three fifths of the
-// time with heads of 64, a third with 128) and by the hand-offs between a row tile's softmax and its two
-// products, 110 to 220 cycles each way, which two row tiles and two buffers hide only in part; a CTA's
-// start and end (10 us, one CTA an SM) weigh on short key ranges. A probe without the exponentials was 13
-// percent faster with heads of 64 and no faster with 128. With Q in shared memory it took 3.8 ms (772 TFLOP/s
+// 870 TFLOP/s, 980 with whole waves of CTAs. Bound by the hand-offs between a row tile's softmax and its two
+// products, 110 to 220 cycles each way, which two row tiles and two buffers hide only in part: a probe without
+// the exponentials (16 a clock and SM, three fifths of the time with heads of 64, a third with 128) was 13
+// percent faster with heads of 64 and no faster with 128. A CTA's start and end (10 us, one CTA an SM) weigh on
+// short key ranges. Where a block of values 2^100 larger sends the CTAs of 1350 tokens over 17776 keys to the
+// row-by-row form, the call takes 72 ms instead of 0.37. With Q in shared memory it took 3.8 ms (772 TFLOP/s
 // with heads of 128), with one score buffer besides 5.4. Tried and not kept: a second thread that issues MMAs, a
 // fifth slower with 128; the two softmax groups taking turns and scores loaded a step ahead in registers, no
 // faster; two threads a row, 535 TFLOP/s; the running maximum behind the exponentials, 622 (with heads of 128
