@@ -510,7 +510,7 @@ typedef struct {
 
 /* Bytes of workspace that serve every sb_kv8_attention call with at most these sizes (batch, heads_q and n_q, any
  * number of key heads, any capacity and window): 5 MB, or up to 16 FP32 copies of the output, but no more than
- * 131 MB. It never falls as a size grows, so one workspace serves a prompt and the tokens behind it.
+ * 137 MB. It never falls as a size grows, so one workspace serves a prompt and the tokens behind it.
  * sb_kv8_store needs 256; batch * heads_q * n_q at most 2^40. Zero it with sb_workspace_init before its first use. */
 sb_status sb_kv8_workspace_size(int64_t batch, int64_t heads_q, int64_t n_q, int32_t dim, size_t* bytes /* host */);
 

@@ -232,3 +232,51 @@ def test_one_workspace_for_a_prompt_and_its_tokens(sbg):
         sbg.check(ws)
         sbg.kv8_attention(q, p.gpu, own, causal=True, ws=sbg.AttnWorkspace(B, Hq, n, 64))
         assert torch.equal(out, own)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 3, 8, 40, 150])
+def test_wide_scales_and_nan_over_parts_of_a_long_cache(sbg, n, D):
+    """Long caches, whose keys are read in parts that are joined: blocks 2^200 apart, zeros among them, shared key heads,
+    and a NaN at a position that only the last query sees."""
+    held = [8100, 700]
+    p = Pair(sbg, 2, 2, 8192, D)
+    k, v = heads(2, 8100, 2, D, 1), heads(2, 8100, 2, D, 2).float()
+    v[0, 4096:4160] *= 2.0 ** 100
+    v[0, 6400:6464] *= 2.0 ** -100
+    v[0, 2048:3072] = 0
+    v[1, 64:128] *= 2.0 ** -90
+    v = v.to(torch.bfloat16)
+    p.store(k, v, counts=held)
+    q = heads(2, n, 4, D, 3)
+    attend(sbg, p, q, causal=True)
+    attend(sbg, p, q, causal=True, window=2500, sinks=5)
+    v[0, 8099, 1, 9] = float("nan")
+    sbg.kv8_store(k, v, p.gpu, start=torch.zeros(2, dtype=torch.int32, device="cuda"),
+                  counts=torch.tensor(held, dtype=torch.int32, device="cuda"), ws=p.ws)
+    with pytest.raises(sbg.SixbitError):
+        sbg.check(p.ws)
+    refer(p)
+    p.ref.codes[1][0, 1, 8099, 9] = 0
+    mark = np.zeros((2, n, 4, D), bool)
+    mark[0, n - 1, 2:, 9] = True
+    attend(sbg, p, q, causal=True, nan=mark)
+
+
+@pytest.mark.parametrize("n", [1, 200])
+def test_rows_computed_apart_in_a_replayed_graph(sbg, n):
+    p = Pair(sbg, 1, 1, 512, 64)
+    stepped(p, [0, -100, 0, 90], [0, 0, 0, 0], 11)
+    q = heads(1, n, 1, 64, 5)
+    out, want, ws = torch.empty_like(q), torch.empty_like(q), sbg.AttnWorkspace(1, 1, n, 64)
+    sbg.kv8_attention(q, p.gpu, want, causal=True, ws=ws)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        sbg.kv8_attention(q, p.gpu, out, causal=True, ws=ws)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        sbg.check(ws)
+        assert torch.equal(out, want)
+    attend(sbg, p, q, causal=True)
