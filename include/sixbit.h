@@ -548,7 +548,8 @@ typedef struct {
  * are FP32. Scales of any spread are sound; a head whose values differ by more than 2^64 from block to block may
  * take some hundred times longer where there are more than 16 query rows for a key head. A NaN
  * that was stored (sb_kv8_store reports it) makes its channel of the queries that see it NaN, in a key all channels,
- * and reaches no others; a head with values from 1.75 * 2^127 on, which may be one, is slower in the same way.
+ * and reaches no others; a head with values from 1.75 * 2^127 on, which may be one, is slower in the same way. (A NaN
+ * code that the caller wrote under a smaller exponent may reach every query of its head.)
  * Inference only: no gradient is computed.
  * lens or q_lens out of range are clamped and SB_ESHAPE is reported by sb_check. ws_bytes: size of ws
  * (SB_ESHAPE if too small). */

@@ -523,9 +523,9 @@ cudaError_t launch_fp8_gemm(const Fp8Linear& L, cudaStream_t s, const char** why
   // hidden). What it decides, measured in us (pair form with 64 / 128 columns, single form with 64 / 128 /
   // 192): 128 x 7680 14.1 / 11.6, 10.0 / 11.1 / 13.2; 226 x 1920 10.1 / 10.9, 9.5 / 10.6 / 12.7;
   // 300 x 7680 21.4 / 15.5, 17.4 / 15.4 / 13.7; 600 x 1920 13.8 / 11.1, 12.9 / 10.6 / 12.6; with 1350 x
-  // 5760 the pair form's 64 / 128 / 192 / 256 columns take 41.0 / 28.7 / 26.6 / 24.6. The order holds at other K: with
-  // K = 256 and 7680, thirteen sizes of 64 to 4096 rows, what it picks is the fastest of the seven or within 1 us of it,
-  // but for 1350 x 1920 x 256 (12.4, single form with 192 columns 10.2) and 4096 x 7680 x 7680 (171, pair form with
+  // 5760 the pair form's 64 / 128 / 192 / 256 columns take 41.0 / 28.7 / 26.6 / 24.6. The order holds at other
+  // K: with K = 256 and 7680, thirteen sizes of 64 to 4096 rows, what it picks is the fastest of the seven or
+  // within 1 us of it, but for 1350 x 1920 x 256 (12.4, single form with 192 columns 10.2) and 4096 x 7680 x 7680 (171, pair form with
   // 256 columns 160).
   static const struct { int cg, bn, ns; } kForms[] = {{2, 256, 6550}, {2, 192, 4980}, {2, 128, 4250}, {2, 64, 3680},
                                                       {1, 192, 7000}, {1, 128, 4500}, {1, 64, 3600}};

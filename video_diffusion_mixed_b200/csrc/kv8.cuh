@@ -81,7 +81,9 @@ __device__ __forceinline__ float far_base(RowStats& r, float top, float c) {
 
 // The factor of a sum of shifted weights of a block `d` below e (at most kFar; what is 2^-119 times a weight
 // adds nothing).
-__device__ __forceinline__ float sum_factor(int d) { return __uint_as_float((uint32_t)(max(d, -119) - kShift + 127) << 23); }
+__device__ __forceinline__ float sum_factor(int d) {
+  return __uint_as_float((uint32_t)(max(d, -119) - kShift + 127) << 23);
+}
 
 // The outputs' unit 2^(e - kShift), e relative to exponent byte e0, as two factors; the reciprocal of l goes
 // between them, and no product on the way leaves the normal range.
@@ -148,8 +150,9 @@ struct ExactRow {
   float lse2;
 };
 template <int D>
-__device__ __forceinline__ void exact_row(const Kv8Attn& p, int64_t b, int64_t hk, int64_t tok, int64_t hq, int len, int pos,
-                                       KeyTiles kt, int size, int i0, int i1, float* qs, ExactRow<D>& out) {
+__device__ __forceinline__ void exact_row(const Kv8Attn& p, int64_t b, int64_t hk, int64_t tok, int64_t hq, int len,
+                                          int pos, KeyTiles kt, int size, int i0, int i1, float* qs,
+                                          ExactRow<D>& out) {
   constexpr int kE = D / 32;
   const int lane = threadIdx.x & 31;
   const int64_t head = b * p.c.heads + hk;

@@ -526,7 +526,10 @@ __global__ void __launch_bounds__(kFewThreads) k_kv8_few(const __grid_constant__
         if (c == 0) *few_part_lse(part, D, gridDim.x, blockIdx.x, side, r) = lse2;
       }
     }
-    if (again) few_redo<D>(p, b, hk, kt, i0, i1, tiles, reinterpret_cast<float*>(ss + kFewWarps * kRows) + warp * D, part);
+    if (again) {
+      float* qs = reinterpret_cast<float*>(ss + kFewWarps * kRows) + warp * D;
+      few_redo<D>(p, b, hk, kt, i0, i1, tiles, qs, part);
+    }
     at += i1 - i0;
     if (!deal || at >= at_end) break;
     fence_proxy_async_smem();  // the join's memory is the ring's again
@@ -653,7 +656,8 @@ static bool cache_map(CUtensorMap* m, const uint8_t* base, const sb_kv8& c) {
 template <int D, int NT>
 static cudaError_t launch_few(const Kv8Attn& p, int deal, unsigned grid, float* part, cudaStream_t s) {
   constexpr int kBytes = few_smem<D>() + 1024;  // + alignment of the dynamic base
-  static_assert(kFewSlots * kFewWarps * 2 * kStep * D >= kFewWarps * (8 * NT * ((int)sizeof(RowStats) + 4 * (D + 4)) + 4 * D),
+  static_assert(kFewSlots * kFewWarps * 2 * kStep * D >=
+                    kFewWarps * (8 * NT * ((int)sizeof(RowStats) + 4 * (D + 4)) + 4 * D),
                 "the join fits the ring");
   static std::atomic<uint64_t> attr{0};
   const cudaError_t e = smem_attr_once(k_kv8_few<D, NT>, kBytes, attr);

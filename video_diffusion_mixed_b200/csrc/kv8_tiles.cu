@@ -13,11 +13,11 @@
 // the keys' enters c, the values' exponent ev the exponent of w, and with it the running maximum, which is
 // that of what w V sums; the row sum takes it out again by an exact factor (RowStats in kv8.cuh). A block of
 // values 2^64 below the largest before it is left out of the product, and if it holds anything but zeros, or if
-// a block may hold a NaN, the CTA computes its rows again one by one in FP32: a branch for that in the softmax's loop, taken or not, cost a
-// tenth of the time of 17776 x 17776, a second loop behind it as much. Queries are scaled by a power of two to
-// [2^14, 2^15) and rounded to fp16, exact for every component within 2^-31 of the row's largest. The maximum
-// moves only when it would rise by more than 2^8, so the accumulator is rescaled rarely; the rest of fp16's
-// range, 2^7, is given to small weights.
+// a block may hold a NaN, the CTA computes its rows again one by one in FP32: a branch for that in the
+// softmax's loop, taken or not, cost a tenth of the time of 17776 x 17776, a second loop behind it as much.
+// Queries are scaled by a power of two to [2^14, 2^15) and rounded to fp16, exact for every component within
+// 2^-31 of the row's largest. The maximum moves only when it would rise by more than 2^8, so the accumulator is
+// rescaled rarely; the rest of fp16's range, 2^7, is given to small weights.
 //
 // Warps: 0-3 and 4-7 softmax of the two row tiles, 8-11 codes -> fp16, 12 MMA issue. A key tile is taken in
 // two steps of 64 keys (a scale block each); the weights overwrite their scores. The shared memory that
@@ -152,7 +152,8 @@ __device__ __forceinline__ uint32_t tile_addr(uint32_t base, int row, int c) {
 // is behind the scores just read, so the parity is not ambiguous.
 template <int D>
 __device__ __forceinline__ bool rescale(TileShared& sh, int t, int u, uint32_t o_col, float f) {
-  if (!__all_sync(0xffffffffu, mbar_wait_bounded(&sh.o_done[t], (uint32_t)((u - 1) & 1), &sh.abort, kWaitNs))) return false;
+  const bool done = mbar_wait_bounded(&sh.o_done[t], (uint32_t)((u - 1) & 1), &sh.abort, kWaitNs);
+  if (!__all_sync(0xffffffffu, done)) return false;
   tc_fence_after();
 #pragma unroll 1
   for (int h = 0; h < D / 16; ++h) {
