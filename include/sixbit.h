@@ -544,7 +544,8 @@ typedef struct {
  * products exactly, queries exactly unless a component is more than 2^31 below its row's largest. For the
  * second product a softmax weight is rounded to fp16 together with its block's scale of V: with P the largest such
  * product of the keys that the row sees, by half a step (2^-11 of itself) down to 2^-21 P and by 2^-32 P below, so
- * that n keys of less weight are lost up to n 2^-32 P. The row's sum and lse count every weight in full; all sums
+ * that n keys of less weight are lost up to n 2^-32 P (a block of zeros counts in P with up to 2^-64 of the head's
+ * largest scale). The row's sum and lse count every weight in full; all sums
  * are FP32. Scales of any spread are sound; a head whose values differ by more than 2^64 from block to block may
  * take some hundred times longer where there are more than 16 query rows for a key head. A NaN
  * that was stored (sb_kv8_store reports it) makes its channel of the queries that see it NaN, in a key all channels,

@@ -15,7 +15,8 @@ def attention(cache, q, nqs, scale, causal=False, window=0, sinks=0, gain=32):
            for what is of second order;
       2^-11  the weight in fp16, half a step; and `sub`: weights times their block's scale are rounded relative
            to the row's largest such product P, so one below 2^-gain P may be lost whole, and one below
-           2^(11 - gain) P is off by at most 2^-gain P;
+           2^(11 - gain) P is off by at most 2^-gain P. A block of zeros has no scale of its own; it stands with
+           at most 2^-64 of the largest, because sums of weights are held within 2^64 of one another;
       2^-12  FP32 sums: at most 1024 steps into one accumulator, 2^-22 each;
       2^-8   the bf16 output, half a step, and 2^-133 below its normal range.
 
@@ -48,7 +49,9 @@ def attention(cache, q, nqs, scale, causal=False, window=0, sinks=0, gain=32):
             e = np.where(p > 0, e, 0.0)
             out[b, :r, h] = p @ v
             lse[b, h, :r] = np.where(live, top + np.log(tot1), -np.inf)[:, 0]
-            prod = np.where(see, (x - top) / np.log(2) + ev, -np.inf)  # log2 of weight times scale
+            zeros = ~(np.add.reduceat(code.sum(1), np.arange(0, held, TOKENS)) > 0).repeat(TOKENS)[:held][None]
+            scale2 = np.where(zeros, np.maximum(ev, ev.max() - 64), ev)
+            prod = np.where(see, (x - top) / np.log(2) + scale2, -np.inf)  # log2 of weight times scale
             P = prod.max(1, keepdims=True)
             lost = see & (prod < P - gain)
             part = see & ~lost & (prod < P - gain + 11)

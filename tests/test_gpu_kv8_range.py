@@ -280,3 +280,21 @@ def test_rows_computed_apart_in_a_replayed_graph(sbg, n):
         sbg.check(ws)
         assert torch.equal(out, want)
     attend(sbg, p, q, causal=True)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 20, 300])
+def test_blocks_of_zeros(sbg, n, D):
+    """First, in between, last and with nearly all the weight: zeros count in the sum and in nothing else."""
+    for zeros, nats in (([0], 0), ([1, 2], 30), ([0, 3, 6], 60), ([6], 110), ([0, 1, 2, 3, 4, 5, 6], 0)):
+        p = Pair(sbg, 1, 1, 512, D)
+        k, v = heads(1, 440, 1, D, 7, 0.3), heads(1, 440, 1, D, 8)
+        k[..., 0] = 0
+        for b in zeros:
+            v[:, 64 * b:64 * b + 64] = 0
+            k[:, 64 * b:64 * b + 64, :, 0] = nats
+        p.store(k, v)
+        q = heads(1, n, 1, D, 9, 0.5)
+        q[..., 0] = 8.0
+        attend(sbg, p, q, causal=True, scale=0.125)
+        attend(sbg, p, q, causal=True, window=130, sinks=2, scale=0.125)

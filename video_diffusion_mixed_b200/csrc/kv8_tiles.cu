@@ -457,8 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = false;
         break;
       }
-      // More than 2^64 below the largest so far, which no row's exponent passes: values of zero are then as good as
-      // theirs, unless they are not zero.
+      // More than 2^64 below the largest so far, which no row's exponent passes: the block stands at 2^-64 with values
+      // of zero, which is right if it holds zeros; if not, the rows are computed again.
       const int floor0 = max(most, ve[0]) - kFar, floor1 = max(most, max(ve[0], ve[1])) - kFar;
       const bool far[2] = {ve[0] < floor0, ve[1] < floor1};
       bool redo = max(ve[0], ve[1]) >= kNanExp;
